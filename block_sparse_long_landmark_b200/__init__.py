@@ -22,6 +22,8 @@ SA_SINK, SA_LOCAL, SA_GATE, SA_HIER, SA_CAUSAL, SA_SELECT_PER_QHEAD = 1, 2, 4, 8
 SA_BF16, SA_FP32 = 0, 1
 SA_OP_LANDMARKS, SA_OP_SELECT, SA_OP_SELECT_DECODE, SA_OP_PREFILL, SA_OP_DECODE = 0, 1, 2, 3, 4
 SA_OP_PREFILL_BACKWARD, SA_OP_SELECT_BACKWARD = 5, 6
+SA_E4M3, SA_INT8 = 0, 1
+SA_OP_PAGED_TABLES, SA_OP_PAGED_APPEND, SA_OP_PAGED_GATHER, SA_OP_PAGED_DECODE, SA_OP_PAGED_PREFILL = 0, 1, 2, 3, 4
 SA_OK, SA_ERR_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE, SA_ERR_LAUNCH, SA_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 
 # SPARSE_ATTN_LIB selects another build of the same library (for example the
@@ -39,6 +41,8 @@ EXPORTS = (
     "sparse_attn_lsa_clusters", "sparse_attn_lsa_workspace_size", "sparse_attn_lsa_build", "sparse_attn_lsa_decode",
     "sparse_attn_lsa_tree_size", "sparse_attn_lsa_tree_workspace_size", "sparse_attn_lsa_tree_build",
     "sparse_attn_lsa_tree_decode",
+    "sparse_attn_paged_workspace_size", "sparse_attn_paged_tables", "sparse_attn_paged_append",
+    "sparse_attn_paged_gather", "sparse_attn_paged_decode", "sparse_attn_paged_prefill",
 )
 
 
@@ -56,6 +60,13 @@ class sa_lsa_params(ctypes.Structure):
                 ("N", ctypes.c_int), ("pool", ctypes.c_int), ("seg", ctypes.c_int), ("clusters", ctypes.c_int),
                 ("top_clusters", ctypes.c_int), ("sink", ctypes.c_int), ("window", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class sa_paged_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("block", ctypes.c_int), ("pages", ctypes.c_int), ("max_blocks", ctypes.c_int),
+                ("tokens", ctypes.c_int), ("top_k", ctypes.c_int), ("flags", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("code", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class SparseAttnError(RuntimeError):
@@ -134,6 +145,16 @@ def lib() -> ctypes.CDLL:
             L.sparse_attn_lsa_tree_build.restype = i
             L.sparse_attn_lsa_tree_decode.argtypes = [LP, i, i] + [vp] * 12 + [sz, vp]
             L.sparse_attn_lsa_tree_decode.restype = i
+            PP, ll = ctypes.POINTER(sa_paged_params), ctypes.c_longlong
+            L.sparse_attn_paged_workspace_size.argtypes = [PP, i]
+            L.sparse_attn_paged_workspace_size.restype = sz
+            L.sparse_attn_paged_tables.argtypes = [PP] + [vp] * 9 + [sz, vp]
+            L.sparse_attn_paged_append.argtypes = [PP, vp, vp, ll, ll] + [vp] * 9 + [sz, vp]
+            L.sparse_attn_paged_gather.argtypes = [PP] + [vp] * 7 + [ll, ll, vp, sz, vp]
+            L.sparse_attn_paged_decode.argtypes = [PP] + [vp] * 13 + [sz, vp]
+            L.sparse_attn_paged_prefill.argtypes = [PP] + [vp] * 11 + [sz, vp]
+            for n in ("tables", "append", "gather", "decode", "prefill"):
+                getattr(L, "sparse_attn_paged_" + n).restype = i
             L.sparse_attn_launch_count.argtypes = []
             L.sparse_attn_launch_count.restype = ctypes.c_ulonglong
             _lib = L
@@ -242,6 +263,39 @@ def sparse_attn_decode_varlen(p, q, K, V, seq_len, idx, score, count, o, lse, ws
 def sparse_attn_decode_step(p, q, L, K, V, seq_len, idx, score, count, o, lse, ws, ws_bytes, stream) -> int:
     return lib().sparse_attn_decode_step(ctypes.byref(p), q, L, K, V, seq_len, idx, score, count, o, lse, ws,
                                          ws_bytes, stream)
+
+
+def sparse_attn_paged_workspace_size(p: sa_paged_params, op: int) -> int:
+    return int(lib().sparse_attn_paged_workspace_size(ctypes.byref(p), op))
+
+
+def sparse_attn_paged_tables(p, cur_len, new_len, free_pages, n_free, n_free_out, table, cu, slot, ws, ws_bytes,
+                             stream) -> int:
+    return lib().sparse_attn_paged_tables(ctypes.byref(p), cur_len, new_len, free_pages, n_free, n_free_out, table,
+                                          cu, slot, ws, ws_bytes, stream)
+
+
+def sparse_attn_paged_append(p, K, V, tok_stride, head_stride, slot, cu, new_len, K8, V8, kscale, vscale, L, ws,
+                             ws_bytes, stream) -> int:
+    return lib().sparse_attn_paged_append(ctypes.byref(p), K, V, tok_stride, head_stride, slot, cu, new_len, K8, V8,
+                                          kscale, vscale, L, ws, ws_bytes, stream)
+
+
+def sparse_attn_paged_gather(p, slot, K8, V8, kscale, vscale, K, V, tok_stride, head_stride, ws, ws_bytes,
+                             stream) -> int:
+    return lib().sparse_attn_paged_gather(ctypes.byref(p), slot, K8, V8, kscale, vscale, K, V, tok_stride,
+                                          head_stride, ws, ws_bytes, stream)
+
+
+def sparse_attn_paged_decode(p, q, K8, V8, kscale, vscale, table, seq_len, idx, score, count, o, lse, ws, ws_bytes,
+                             stream) -> int:
+    return lib().sparse_attn_paged_decode(ctypes.byref(p), q, K8, V8, kscale, vscale, table, seq_len, idx, score,
+                                          count, o, lse, ws, ws_bytes, stream)
+
+
+def sparse_attn_paged_prefill(p, Q, cu, K8, V8, kscale, vscale, table, seq_len, O, lse, ws, ws_bytes, stream) -> int:
+    return lib().sparse_attn_paged_prefill(ctypes.byref(p), Q, cu, K8, V8, kscale, vscale, table, seq_len, O, lse,
+                                           ws, ws_bytes, stream)
 
 
 def sparse_attn_check_status(ws, stream):
@@ -545,6 +599,164 @@ def lsa_tree_decode(p: sa_lsa_params, fanout: int, beam: int, q, K, V, index, tr
                                        _ptr(sizes), _ptr(tree), _ptr(o), _ptr(lse), _ptr(kept), _ptr(compared),
                                        _ptr(ws), ws.numel(), _stream(stream)), "sparse_attn_lsa_tree_decode")
     return o, lse
+
+
+# ---- paged 8-bit cache: tensors are checked for type, size, density and
+# device, and the call runs on their device's current stream ----------------
+
+def make_paged_params(B, Hq, Hkv, d, block, pages, max_blocks, tokens=0, top_k=0, flags=0, dtype="bf16", code="e4m3",
+                      scale=0.0) -> sa_paged_params:
+    dt = {"bf16": SA_BF16, "fp32": SA_FP32}.get(dtype, dtype)
+    cd = {"e4m3": SA_E4M3, "int8": SA_INT8}.get(code, code)
+    return sa_paged_params(B, Hq, Hkv, d, block, pages, max_blocks, tokens, top_k, flags, dt, cd, float(scale))
+
+
+def paged_workspace(p: sa_paged_params, device="cuda", ops=None):
+    """A zero-filled workspace for the paged operations `ops` of `p`
+    (SA_OP_PAGED_* codes; every one when None)."""
+    n = max(sparse_attn_paged_workspace_size(p, op) for op in (range(5) if ops is None else ops))
+    if n == 0:
+        raise SparseAttnError(SA_ERR_ARG, "sparse_attn_paged_workspace_size")
+    return _torch().zeros(n, dtype=_torch().uint8, device=device)
+
+
+def paged_cache(p: sa_paged_params, device="cuda"):
+    """An empty cache: (codes of K, codes of V, scales of K, scales of V)."""
+    torch = _torch()
+    ct = torch.float8_e4m3fn if p.code == SA_E4M3 else torch.int8
+    shape = (p.pages, p.Hkv, p.block, p.d)
+    return (torch.zeros(shape, dtype=torch.uint8, device=device).view(ct),
+            torch.zeros(shape, dtype=torch.uint8, device=device).view(ct),
+            torch.zeros(shape[:2], dtype=torch.float32, device=device),
+            torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+
+def _same(what, device, *checks):
+    """Refuses a tensor of another type, size or device, or one that is not dense."""
+    for name, t, dtype, numel in checks:
+        if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+            raise SparseAttnError(SA_ERR_ARG, f"{what}: {name} must be a dense {dtype} tensor of {numel} elements on "
+                                              f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _cache_checks(p, cache):
+    torch = _torch()
+    K8, V8, ks, vs = cache
+    ct = torch.float8_e4m3fn if p.code == SA_E4M3 else torch.int8
+    n = p.pages * p.Hkv
+    return (("K codes", K8, ct, n * p.block * p.d), ("V codes", V8, ct, n * p.block * p.d),
+            ("K scales", ks, torch.float32, n), ("V scales", vs, torch.float32, n))
+
+
+def _on(device, stream, fn, *args):
+    """Runs fn(*args, stream) with `device` current."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _row_strides(what, p, K, V):
+    """(token, head) strides of packed rows [tokens, Hkv, d] whose last
+    dimension is dense; K and V alike."""
+    dt = _tdtype(p)
+    for t in (K, V):
+        if t.dtype != dt or tuple(t.shape) != (p.tokens, p.Hkv, p.d) or t.device != K.device or \
+                (t.numel() and (t.stride() != K.stride() or t.stride(2) != 1)):
+            raise SparseAttnError(SA_ERR_ARG, f"{what}: K and V must be {dt} [{p.tokens}, {p.Hkv}, {p.d}] with the same "
+                                              "strides and a dense last dimension")
+    hs = K.stride(1) if p.Hkv > 1 else p.d
+    return (K.stride(0) if p.tokens > 1 else p.Hkv * hs), hs
+
+
+def paged_tables(p: sa_paged_params, cur_len, new_len, free_pages, n_free, table, ws, out=None, stream=None):
+    """Block table (in place) and slot map of a step: (n_free, cu, slot)."""
+    torch = _torch()
+    dev, i32 = table.device, torch.int32
+    if out is None:
+        out = (torch.empty(1, dtype=i32, device=dev), torch.empty(p.B + 1, dtype=i32, device=dev),
+               torch.empty(p.tokens, dtype=torch.int64, device=dev))
+    n_out, cu, slot = out
+    _same("paged_tables", dev, ("cur_len", cur_len, i32, p.B), ("new_len", new_len, i32, p.B),
+          ("free_pages", free_pages, i32, p.pages), ("n_free", n_free, i32, 1), ("table", table, i32, p.B * p.max_blocks),
+          ("n_free_out", n_out, i32, 1), ("cu", cu, i32, p.B + 1), ("slot", slot, torch.int64, p.tokens))
+    _check(_on(dev, stream, sparse_attn_paged_tables, p, _ptr(cur_len), _ptr(new_len), _ptr(free_pages), _ptr(n_free),
+               _ptr(n_out), _ptr(table), _ptr(cu), _ptr(slot), _ptr(ws), ws.numel()), "sparse_attn_paged_tables")
+    return out
+
+
+def paged_append(p: sa_paged_params, K, V, slot, cache, ws, cu=None, new_len=None, L=None, stream=None):
+    """Quantises K, V [tokens, Hkv, d] (strided rows allowed) into the cache at
+    `slot`; with L, cu and new_len also the landmarks of the touched blocks."""
+    torch = _torch()
+    dev = cache[0].device
+    ts, hs = _row_strides("paged_append", p, K, V)
+    checks = _cache_checks(p, cache) + (("slot", slot, torch.int64, p.tokens),)
+    if L is not None:
+        if cu is None or new_len is None:
+            raise SparseAttnError(SA_ERR_ARG, "paged_append: landmarks need cu and new_len")
+        checks += (("L", L, _tdtype(p), p.B * p.Hkv * p.max_blocks * p.d), ("cu", cu, torch.int32, p.B + 1),
+                   ("new_len", new_len, torch.int32, p.B))
+    if K.device != dev:
+        raise SparseAttnError(SA_ERR_ARG, f"paged_append: K and V must be on {dev}")
+    _same("paged_append", dev, *checks)
+    _check(_on(dev, stream, sparse_attn_paged_append, p, _ptr(K), _ptr(V), ts, hs, _ptr(slot), _ptr(cu),
+               _ptr(new_len), *map(_ptr, cache), _ptr(L), _ptr(ws), ws.numel()), "sparse_attn_paged_append")
+    return cache
+
+
+def paged_gather(p: sa_paged_params, slot, cache, ws, out=None, stream=None):
+    """The cached keys and values at `slot`: (K, V) [tokens, Hkv, d]."""
+    torch = _torch()
+    dev = cache[0].device
+    if out is None:
+        out = tuple(torch.empty(p.tokens, p.Hkv, p.d, dtype=_tdtype(p), device=dev) for _ in "kv")
+    ts, hs = _row_strides("paged_gather", p, *out)
+    _same("paged_gather", dev, *_cache_checks(p, cache), ("slot", slot, torch.int64, p.tokens))
+    if out[0].device != dev:
+        raise SparseAttnError(SA_ERR_ARG, f"paged_gather: K and V must be on {dev}")
+    _check(_on(dev, stream, sparse_attn_paged_gather, p, _ptr(slot), *map(_ptr, cache), _ptr(out[0]), _ptr(out[1]),
+               ts, hs, _ptr(ws), ws.numel()), "sparse_attn_paged_gather")
+    return out
+
+
+def paged_decode(p: sa_paged_params, q, cache, table, seq_len, ws, lists=None, out=None, stream=None):
+    """One query per sequence over the cache: (o, lse).  lists = (idx, score,
+    count) of select_decode_varlen, or None for every block."""
+    torch = _torch()
+    dev, i32 = cache[0].device, torch.int32
+    if out is None:
+        out = (torch.empty_like(q), torch.empty(p.B, p.Hq, dtype=torch.float32, device=dev))
+    o, lse = out
+    n, dt = p.B * p.Hq, _tdtype(p)
+    checks = _cache_checks(p, cache) + (("q", q, dt, n * p.d), ("o", o, dt, n * p.d), ("lse", lse, torch.float32, n),
+                                        ("table", table, i32, p.B * p.max_blocks), ("seq_len", seq_len, i32, p.B))
+    idx, sc, cnt = lists if lists is not None else (None, None, None)
+    if lists is not None:
+        u = p.B * _hsel(p)
+        checks += (("idx", idx, i32, u * (p.top_k + 2)), ("score", sc, torch.float32, u * (p.top_k + 2)),
+                   ("count", cnt, i32, u))
+    _same("paged_decode", dev, *checks)
+    _check(_on(dev, stream, sparse_attn_paged_decode, p, _ptr(q), *map(_ptr, cache), _ptr(table), _ptr(seq_len),
+               _ptr(idx), _ptr(sc), _ptr(cnt), _ptr(o), _ptr(lse), _ptr(ws), ws.numel()), "sparse_attn_paged_decode")
+    return out
+
+
+def paged_prefill(p: sa_paged_params, Q, cu, cache, table, seq_len, ws, out=None, stream=None):
+    """Packed query chunks [tokens, Hq, d] over the cache: (O, lse [tokens, Hq])."""
+    torch = _torch()
+    dev, i32 = cache[0].device, torch.int32
+    if out is None:
+        out = (torch.empty_like(Q), torch.empty(p.tokens, p.Hq, dtype=torch.float32, device=dev))
+    O, lse = out
+    n, dt = p.tokens * p.Hq, _tdtype(p)
+    _same("paged_prefill", dev, *_cache_checks(p, cache), ("Q", Q, dt, n * p.d), ("O", O, dt, n * p.d),
+          ("lse", lse, torch.float32, n), ("cu", cu, i32, p.B + 1), ("table", table, i32, p.B * p.max_blocks),
+          ("seq_len", seq_len, i32, p.B))
+    _check(_on(dev, stream, sparse_attn_paged_prefill, p, _ptr(Q), _ptr(cu), *map(_ptr, cache), _ptr(table),
+               _ptr(seq_len), _ptr(O), _ptr(lse), _ptr(ws), ws.numel()), "sparse_attn_paged_prefill")
+    return out
 
 
 def lsa_tree_levels(p: sa_lsa_params, fanout: int, tree):

@@ -121,13 +121,13 @@ int resolve_lsa(const sa_lsa_params *p, LsaShape &s) {
 
 thread_local int t_last_cuda_error = 0;
 
-int launch_result(cudaError_t e) {
+}  // namespace
+
+int sa::launch_result(cudaError_t e) {
     if (e == cudaSuccess) return SA_OK;
     t_last_cuda_error = (int)e;
     return SA_ERR_LAUNCH;
 }
-
-}  // namespace
 
 // Decode on a fixed scratch buffer (the no-allocation entry point): the
 // status word, the per-unit completion counters and this call's split

@@ -168,6 +168,10 @@ int decode_on_scratch(const sa_params *p, const void *q, const void *K, const vo
 // Process-wide count of kernels this library has launched (for reporting).
 void note_launch();
 
+// The return code of a launch; a failure's cudaError_t is kept for
+// sparse_attn_last_cuda_error.
+int launch_result(cudaError_t e);
+
 // Streaming multiprocessors of the current device (0 on failure).
 int sm_count();
 

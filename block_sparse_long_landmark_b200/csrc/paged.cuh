@@ -1,0 +1,98 @@
+// paged.cuh -- shared pieces of the paged 8-bit key/value cache: the resolved
+// shape of a call, code <-> value conversions, and the internal launchers.
+//
+// A page holds `bs` tokens of every kv-head: codes [pages][Hkv][bs][d], one
+// byte each, and one fp32 scale per (page, head) for the keys and one for the
+// values.  A cached value is code * scale.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace sa {
+
+// Status bits of the paged calls besides those of common.cuh.
+constexpr unsigned kStatusPool = 16u;   // block tables: pages or slots ran out
+
+struct PagedShape {
+    int B, Hq, Hkv, G, d, bs, pages, maxb, tokens, cap, flags, dtype, code;
+    int Hsel;        // heads that own a kept list (Hkv, or Hq with SA_SELECT_PER_QHEAD)
+    int heads_per;   // query heads that share one list
+    float scale;
+};
+
+// Cache length of sequence b, clamped to [0, maxb * bs].
+__device__ __forceinline__ int paged_len(const PagedShape &s, const int32_t *seq_len, int b) {
+    return min(max(seq_len[b], 0), s.maxb * s.bs);
+}
+
+// An e4m3 code as fp32.  Moving sign and the seven value bits into an fp16
+// gives the value / 256 exactly, subnormal codes included; the two NaN codes,
+// which the append never writes, read as +-480.
+__device__ __forceinline__ float e4m3_value(unsigned c) {
+    const unsigned short h = (unsigned short)(((c & 0x80u) << 8) | ((c & 0x7fu) << 7));
+    return __half2float(__ushort_as_half(h)) * 256.f;
+}
+template <int kCode>
+__device__ __forceinline__ float code_value(unsigned byte) {
+    return kCode == SA_E4M3 ? e4m3_value(byte) : (float)(signed char)byte;
+}
+// Four codes of one word, in byte order.
+template <int kCode>
+__device__ __forceinline__ void code_values4(uint32_t w, float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = code_value<kCode>((w >> (8 * i)) & 0xffu);
+}
+// Two finite values rounded to codes (nearest, ties to even; saturating), the
+// first in the low byte.
+template <int kCode>
+__device__ __forceinline__ uint32_t codes_of2(float a, float b) {
+    if (kCode == SA_E4M3) {
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+        return r;
+    }
+    const int x = __float2int_rn(fminf(fmaxf(a, -127.f), 127.f));
+    const int y = __float2int_rn(fminf(fmaxf(b, -127.f), 127.f));
+    return (uint32_t)(x & 0xff) | ((uint32_t)(y & 0xff) << 8);
+}
+
+// Workspace of the paged calls: the status word, the decode's completion
+// counters (one per unit and group of 16 heads; zero between calls), then
+// scratch that every call reuses.
+struct PagedWs {
+    size_t cnt;       // decode: [B * Hsel * head groups]
+    size_t scratch;
+};
+PagedWs paged_ws(const PagedShape &s);
+
+cudaError_t launch_paged_tables(const PagedShape &s, const int32_t *cur, const int32_t *want, int32_t *free_pages,
+                                const int32_t *n_free, int32_t *n_free_out, int32_t *table, int32_t *cu,
+                                int64_t *slot, unsigned *status, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedShape &s, const void *K, const void *V, long long tok_stride,
+                                long long head_stride, const int64_t *slot, const int32_t *cu, const int32_t *new_len,
+                                uint8_t *K8, uint8_t *V8, float *ks, float *vs, void *L, unsigned *status,
+                                cudaStream_t st);
+cudaError_t launch_paged_gather(const PagedShape &s, const int64_t *slot, const uint8_t *K8, const uint8_t *V8,
+                                const float *ks, const float *vs, void *K, void *V, long long tok_stride,
+                                long long head_stride, unsigned *status, cudaStream_t st);
+
+// What the attention over the cache reads.
+struct PagedCache {
+    const uint8_t *K, *V;
+    const float *ks, *vs;
+    const int32_t *table;     // [B][maxb]
+    const int32_t *seq_len;   // [B]
+};
+// Kept lists of a decode (idx null: every block of the sequence).
+struct PagedLists {
+    const int32_t *idx;
+    const float *score;
+    const int32_t *count;
+};
+// One query per sequence (cu null), or packed chunk rows (cu given, no lists).
+cudaError_t launch_paged_simt(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
+                              const PagedLists &l, void *o, float *lse, unsigned *status, cudaStream_t st);
+
+}  // namespace sa

@@ -1,0 +1,452 @@
+// paged_cache.cu -- block tables and slot maps, the quantising append and the
+// read-back of the paged 8-bit key/value cache.
+#include "paged.cuh"
+
+namespace sa {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Block tables and slot maps
+//
+// Sequence b grows or shrinks from cur[b] to want[b] tokens.  With nb(x) =
+// ceil(x / bs): a shrinking sequence gives back its blocks nb(want) ..
+// nb(cur) - 1, pushed in order of (sequence, block) on the free stack; a
+// growing one takes nb(want) - nb(cur) pages, popped in the same order.  Pop
+// number a is therefore the released page R - 1 - a while a < R, then
+// free[n_free - 1 - (a - R)]: a function of the inputs alone, so one launch
+// does it all without a word between its CTAs.  Every CTA scans the B
+// lengths into shared memory (a few bytes a sequence, from L2) and takes its
+// share of the slots and of the new table entries, each found by a binary
+// search in the scanned offsets.  Latency bound: two dependent global reads.
+// ---------------------------------------------------------------------------
+constexpr int kTabThreads = 512;
+
+struct Sum3 {
+    int t, a, r;   // new tokens, pages wanted, pages released
+};
+__device__ __forceinline__ Sum3 add3(Sum3 x, Sum3 y) { return {x.t + y.t, x.a + y.a, x.r + y.r}; }
+
+// Last index b in [0, n) with off[b] <= x (off ascending, off[0] = 0).
+__device__ __forceinline__ int owner(const int *off, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (off[m] <= x) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads)
+paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t *__restrict__ want,
+                    int32_t *free_pages, const int32_t *__restrict__ n_free_in, int32_t *n_free_out, int32_t *table,
+                    int32_t *cu, int64_t *slot, unsigned *status) {
+    extern __shared__ int sm_tab[];
+    const int B = s.B, bs = s.bs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *offT = sm_tab, *offA = offT + B + 1, *offR = offA + B + 1;
+    __shared__ Sum3 wsum[kTabThreads / 32];
+    __shared__ int bad_s;
+    __shared__ long long big_s;
+    if (tid == 0) {
+        bad_s = 0;
+        big_s = 0;
+    }
+    __syncthreads();
+    const int per = (B + kTabThreads - 1) / kTabThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int most = s.maxb * bs;
+    Sum3 mine{0, 0, 0};
+    long long tok = 0;   // the sum of new tokens may pass 32 bits; such a call is refused
+    int bad = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int c = cur[b], w = want[b];
+        if (c < 0 || c > most || w < 0 || w > most) {
+            bad = 1;
+            continue;
+        }
+        const int oc = (c + bs - 1) / bs, ow = (w + bs - 1) / bs;
+        tok += max(0, w - c);
+        mine = add3(mine, {max(0, w - c), max(0, ow - oc), max(0, oc - ow)});
+    }
+    if (bad) bad_s = 1;
+    if (tok) atomicAdd(reinterpret_cast<unsigned long long *>(&big_s), (unsigned long long)tok);
+    Sum3 inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum3 y{__shfl_up_sync(~0u, inc.t, o), __shfl_up_sync(~0u, inc.a, o), __shfl_up_sync(~0u, inc.r, o)};
+        if (lane >= o) inc = add3(inc, y);
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    Sum3 base{0, 0, 0}, tot{0, 0, 0};
+    for (int w = 0; w < kTabThreads / 32; ++w) {
+        if (w < warp) base = add3(base, wsum[w]);
+        tot = add3(tot, wsum[w]);
+    }
+    Sum3 at = add3(base, {inc.t - mine.t, inc.a - mine.a, inc.r - mine.r});
+    const int nf = n_free_in[0];
+    const bool wrong = bad_s || nf < 0 || nf > s.pages;
+    const bool out = !wrong && (big_s > s.tokens || tot.a > (long long)nf + tot.r || nf + (long long)tot.r - tot.a > s.pages);
+    const bool refuse = wrong || out;   // nothing changes: no slots, the same free pages
+    for (int b = b0; b < b1; ++b) {
+        const int c = refuse ? 0 : cur[b], w = refuse ? 0 : want[b];
+        const int oc = (c + bs - 1) / bs, ow = (w + bs - 1) / bs;
+        offT[b] = refuse ? 0 : at.t;
+        offA[b] = refuse ? 0 : at.a;
+        offR[b] = refuse ? 0 : at.r;
+        at = add3(at, {max(0, w - c), max(0, ow - oc), max(0, oc - ow)});
+    }
+    const int T = refuse ? 0 : tot.t, A = refuse ? 0 : tot.a, R = refuse ? 0 : tot.r;
+    if (tid == 0) {
+        offT[B] = T;
+        offA[B] = A;
+        offR[B] = R;
+        if (blockIdx.x == 0) {
+            n_free_out[0] = refuse ? nf : nf + R - A;
+            if (wrong) set_status(status, kStatusBadIndex);
+            if (out) set_status(status, kStatusPool);
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= B; b += kTabThreads) cu[b] = offT[b];
+
+    // the i-th page given back, in order of (sequence, block)
+    auto released = [&](int i) {
+        const int b = owner(offR, B, i);
+        return table[(size_t)b * s.maxb + (want[b] + bs - 1) / bs + (i - offR[b])];
+    };
+    // the page of pop number a (-1, with a status, if the list holds none there)
+    auto popped = [&](int a) {
+        const int pg = a < R ? released(R - 1 - a) : free_pages[nf - 1 - (a - R)];
+        if (pg >= 0 && pg < s.pages) return pg;
+        set_status(status, kStatusBadIndex);
+        return -1;
+    };
+    const long long step = (long long)gridDim.x * kTabThreads, first = (long long)blockIdx.x * kTabThreads + tid;
+    for (long long i = first; i < A; i += step) {
+        const int b = owner(offA, B, (int)i);
+        table[(size_t)b * s.maxb + (cur[b] + bs - 1) / bs + ((int)i - offA[b])] = popped((int)i);
+    }
+    // what stays released goes on the stack (above every entry that is popped)
+    for (long long i = first; i < R - A; i += step) free_pages[nf + i] = released((int)i);
+    for (long long i = first; i < s.tokens; i += step) {
+        long long out_slot = -1;
+        if (i < T) {
+            const int b = owner(offT, B, (int)i);
+            const int c = cur[b], pos = c + ((int)i - offT[b]), j = pos / bs, oc = (c + bs - 1) / bs;
+            int pg;
+            if (j < oc) {
+                pg = table[(size_t)b * s.maxb + j];
+                if (pg < 0 || pg >= s.pages) {
+                    set_status(status, kStatusBadIndex);
+                    pg = -1;
+                }
+            } else {
+                pg = popped(offA[b] + j - oc);
+            }
+            if (pg >= 0) out_slot = (long long)pg * bs + pos % bs;
+        }
+        slot[i] = out_slot;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Append
+// ---------------------------------------------------------------------------
+
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) { load16(p, f); }
+__device__ __forceinline__ void load8(const float *p, float *f) {
+    load16(p, f);
+    load16(p + 4, f + 4);
+}
+
+// The smallest power of two s >= 2^-126 with amax <= M s (M = 448 or 127), from
+// the bits of the finite amax: amax = 1.f * 2^x fits M 2^e exactly when
+// 1.f <= 1.75 (e4m3; 1.984375 for int8) at e = x - 8 (x - 6), else one more.
+template <int kCode>
+__device__ __forceinline__ float scale_for(float amax) {
+    const unsigned u = __float_as_uint(amax);
+    const int x = (int)(u >> 23) - 127;
+    const unsigned frac = u & 0x7fffffu;
+    int e = kCode == SA_E4M3 ? x - 8 + (frac > 0x600000u) : x - 6 + (frac > 0x7e0000u);
+    e = max(e, -126);
+    return __uint_as_float((unsigned)(e + 127) << 23);
+}
+
+constexpr int kAppThreads = 256;   // 128 for the keys, 128 for the values
+constexpr int kWinMax = 64;        // tokens whose runs one CTA looks for
+
+// A run: consecutive slots of one page.  The CTA of (window, head) takes the
+// runs that begin in its window: it finds the new rows' largest magnitude,
+// keeps the block's scale when they fit, else takes the power of two that
+// holds them and rounds the codes already there anew (scales are powers of
+// two, so a scaled value is exact and a code is one rounding of it), writes
+// the codes, and means the block's cached keys into its landmark.
+template <typename T, int kCode, int kD>
+__global__ void __launch_bounds__(kAppThreads)
+paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__ V, long long ts, long long hs,
+                    const int64_t *__restrict__ slot, const int32_t *__restrict__ cu,
+                    const int32_t *__restrict__ new_len, uint8_t *K8, uint8_t *V8, float *ks, float *vs, T *L,
+                    int window, unsigned *status) {
+    constexpr int VPR = kD / 8;           // vectors of eight per row
+    constexpr int RS = 128 / VPR;         // rows per step of a half
+    constexpr float kMost = kCode == SA_E4M3 ? 448.f : 127.f;
+    __shared__ int sl[kWinMax + 129];     // slots from the token before the window on
+    __shared__ unsigned brk[(kWinMax + 129 + 31) / 32 + 1];
+    __shared__ float red[2][4];
+    __shared__ float lsum[4][kD];
+    const int tid = threadIdx.x, lane = tid & 31, half = tid >> 7, t = tid & 127, w4 = t >> 5;
+    const int cv = t % VPR, rs = t / VPR;
+    const int h = blockIdx.y, bs = s.bs;
+    const long long w0 = (long long)blockIdx.x * window;
+    const int span = (int)min((long long)window + bs, (long long)s.tokens - w0);   // tokens w0 .. w0 + span - 1
+    // sl[j + 1] = slot of token w0 + j, -1 when there is none or it is out of range
+    if (tid <= span && tid < kWinMax + 129) {
+        const long long i = w0 + tid - 1;
+        const long long x = i >= 0 ? slot[i] : -1;
+        const bool good = x >= 0 && x < (long long)s.pages * bs;
+        if (x >= 0 && !good) set_status(status, kStatusBadIndex);
+        sl[tid] = good ? (int)x : -1;
+    }
+    __syncthreads();
+    {
+        // bit j of brk: a run ends before token w0 + j
+        const int j = tid;
+        const bool b = j >= span || sl[j + 1] < 0 || sl[j + 1] != sl[j] + 1 || sl[j] < 0 || sl[j + 1] % bs == 0;
+        const unsigned m = __ballot_sync(~0u, b);
+        if (lane == 0 && (tid >> 5) < (int)(sizeof(brk) / 4)) brk[tid >> 5] = m;
+    }
+    __syncthreads();
+    const T *src = half ? V : K;
+    uint8_t *codes = half ? V8 : K8;
+    float *scales = half ? vs : ks;
+    for (int j = 0; j < min(window, span); ++j) {
+        const int first = sl[j + 1];
+        if (first < 0 || !((brk[j >> 5] >> (j & 31)) & 1u)) continue;
+        int end = j + 1;                  // next break (a set bit always follows: bits from span on are set)
+        while (!((brk[end >> 5] >> (end & 31)) & 1u)) {
+            const unsigned rest = brk[end >> 5] >> (end & 31);
+            end = rest ? end + __ffs(rest) - 1 : (end | 31) + 1;
+        }
+        const int n = end - j, page = first / bs, off = first - page * bs;
+        const T *x0 = src + (w0 + j) * ts + (long long)h * hs + cv * 8;
+        uint8_t *blk = codes + ((size_t)page * s.Hkv + h) * bs * kD + cv * 8;
+        float *scale_at = scales + (size_t)page * s.Hkv + h;
+        const float was = off > 0 ? *scale_at : 0.f;
+        // largest finite magnitude of the new rows
+        float am = 0.f;
+        bool odd = false;
+        for (int r = rs; r < n; r += RS) {
+            float f[8];
+            load8(x0 + r * ts, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = fabsf(f[i]);
+                const bool fin = m <= 3.402823466e38f;
+                odd |= !fin;
+                am = fin ? fmaxf(am, m) : am;
+            }
+        }
+        if (odd) set_status(status, kStatusNaN);
+        am = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(am)));
+        if (lane == 0) red[half][w4] = am;
+        asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+        am = fmaxf(fmaxf(red[half][0], red[half][1]), fmaxf(red[half][2], red[half][3]));
+        const bool usable = was >= 1.17549435e-38f && was <= 3.402823466e38f;
+        const bool fits = off > 0 && usable && am <= kMost * was;
+        const float now = fits ? was : scale_for<kCode>(am);
+        // a power of two divides exactly by its reciprocal; a kept scale may be any number
+        const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
+        const float inv = __fdiv_rn(1.f, now);
+        const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
+        float acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        // codes already in the block
+        if (!fits || (half == 0 && L)) {
+            for (int r = rs; r < off; r += RS) {
+                uint2 c = *reinterpret_cast<const uint2 *>(blk + (size_t)r * kD);
+                float f[8];
+                code_values4<kCode>(c.x, f);
+                code_values4<kCode>(c.y, f + 4);
+                if (!fits) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] *= ratio;
+                    c.x = codes_of2<kCode>(f[0], f[1]) | codes_of2<kCode>(f[2], f[3]) << 16;
+                    c.y = codes_of2<kCode>(f[4], f[5]) | codes_of2<kCode>(f[6], f[7]) << 16;
+                    *reinterpret_cast<uint2 *>(blk + (size_t)r * kD) = c;
+                    code_values4<kCode>(c.x, f);
+                    code_values4<kCode>(c.y, f + 4);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+            }
+        }
+        // the new rows: NaN becomes 0, infinities the largest code
+        for (int r = rs; r < n; r += RS) {
+            float f[8];
+            load8(x0 + r * ts, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = pow2 ? f[i] * inv : __fdiv_rn(f[i], now);
+                f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(y, -kMost), kMost);
+            }
+            uint2 c;
+            c.x = codes_of2<kCode>(f[0], f[1]) | codes_of2<kCode>(f[2], f[3]) << 16;
+            c.y = codes_of2<kCode>(f[4], f[5]) | codes_of2<kCode>(f[6], f[7]) << 16;
+            *reinterpret_cast<uint2 *>(blk + (size_t)(off + r) * kD) = c;
+            if (half == 0 && L) {
+                code_values4<kCode>(c.x, f);
+                code_values4<kCode>(c.y, f + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+            }
+        }
+        if (t == 0) *scale_at = now;
+        if (half == 0 && L) {
+            // sums of codes are exact in fp32 up to 2^24 steps of 2^-9 (one
+            // rounding at most in a full block of 128 extreme codes)
+            const long long i = w0 + j;
+            const int b = owner(cu, s.B, (int)min(i, (long long)cu[s.B] - 1));
+            const int pos = new_len[b] - cu[b + 1] + (int)i;
+            const bool good = i < cu[s.B] && pos >= 0 && pos % bs == off && pos / bs < s.maxb;
+            if (!good && t == 0) set_status(status, kStatusBadIndex);
+#pragma unroll
+            for (int i2 = 0; i2 < 8; ++i2) {
+#pragma unroll
+                for (int o = VPR; o < 32; o <<= 1) acc[i2] += __shfl_xor_sync(~0u, acc[i2], o);
+            }
+            if (lane < VPR) {
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) lsum[w4][cv * 8 + i2] = acc[i2];
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (good && t < kD) {
+                const float sum = (lsum[0][t] + lsum[1][t]) + (lsum[2][t] + lsum[3][t]);
+                const float mean = __fdiv_rn(sum * now, (float)(off + n));
+                from_f(L[(((size_t)b * s.Hkv + h) * s.maxb + pos / bs) * kD + t], mean);
+            }
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Read-back: row i = the cached keys and values at slot[i] (zeros where the
+// slot is negative or out of range).  One thread per 16 codes of K and of V.
+// ---------------------------------------------------------------------------
+template <typename T, int kCode>
+__global__ void __launch_bounds__(256)
+paged_gather_kernel(PagedShape s, const int64_t *__restrict__ slot, const uint8_t *__restrict__ K8,
+                    const uint8_t *__restrict__ V8, const float *__restrict__ ks, const float *__restrict__ vs, T *K,
+                    T *V, long long ts, long long hs, unsigned *status) {
+    const int vpr = s.d / 16;
+    const long long total = (long long)s.tokens * s.Hkv * vpr;
+    for (long long x = (long long)blockIdx.x * 256 + threadIdx.x; x < total; x += (long long)gridDim.x * 256) {
+        const int c = (int)(x % vpr);
+        const long long y = x / vpr;
+        const int h = (int)(y % s.Hkv);
+        const long long i = y / s.Hkv;
+        const long long sl = slot[i];
+        const bool good = sl >= 0 && sl < (long long)s.pages * s.bs;
+        if (sl >= 0 && !good) set_status(status, kStatusBadIndex);
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        float sk = 0.f, sv = 0.f;
+        if (good) {
+            const int page = (int)(sl / s.bs), off = (int)(sl - (long long)page * s.bs);
+            const size_t ph = (size_t)page * s.Hkv + h;
+            const size_t at = (ph * s.bs + off) * s.d + c * 16;
+            k = *reinterpret_cast<const uint4 *>(K8 + at);
+            v = *reinterpret_cast<const uint4 *>(V8 + at);
+            sk = ks[ph];
+            sv = vs[ph];
+        }
+        T *ok = K + i * ts + h * hs + c * 16, *ov = V + i * ts + h * hs + c * 16;
+        float f[16];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint4 u = half ? v : k;
+            const float sc = half ? sv : sk;
+            code_values4<kCode>(u.x, f);
+            code_values4<kCode>(u.y, f + 4);
+            code_values4<kCode>(u.z, f + 8);
+            code_values4<kCode>(u.w, f + 12);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] *= sc;
+            T *o = half ? ov : ok;
+#pragma unroll
+            for (int e = 0; e < 16; e += Vec<T>::n) store16(o + e, f + e);
+        }
+    }
+}
+
+template <typename T, int kCode>
+cudaError_t append_t(const PagedShape &s, const void *K, const void *V, long long ts, long long hs,
+                     const int64_t *slot, const int32_t *cu, const int32_t *nl, uint8_t *K8, uint8_t *V8, float *ks,
+                     float *vs, void *L, unsigned *status, cudaStream_t st) {
+    // One token per CTA while the CTAs of all (token, head) pairs fit about
+    // one wave of eight per SM (decode steps); longer windows beyond that, so
+    // that a prompt's tokens, of which one in `block` begins a run, do not
+    // cost a CTA each.
+    int window = 1;
+    while (window < kWinMax && (long long)s.tokens * s.Hkv > (long long)window * 8 * max(1, sm_count())) window <<= 1;
+    const dim3 grid((unsigned)((s.tokens + window - 1) / window), s.Hkv);
+    auto k = s.d == 128 ? paged_append_kernel<T, kCode, 128> : paged_append_kernel<T, kCode, 64>;
+    k<<<grid, kAppThreads, 0, st>>>(s, (const T *)K, (const T *)V, ts, hs, slot, cu, nl, K8, V8, ks, vs, (T *)L,
+                                    window, status);
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int kCode>
+cudaError_t gather_t(const PagedShape &s, const int64_t *slot, const uint8_t *K8, const uint8_t *V8, const float *ks,
+                     const float *vs, void *K, void *V, long long ts, long long hs, unsigned *status,
+                     cudaStream_t st) {
+    const long long total = (long long)s.tokens * s.Hkv * (s.d / 16);
+    const unsigned grid = (unsigned)min((total + 255) / 256, 64ll * max(1, sm_count()));
+    paged_gather_kernel<T, kCode><<<grid, 256, 0, st>>>(s, slot, K8, V8, ks, vs, (T *)K, (T *)V, ts, hs, status);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tables(const PagedShape &s, const int32_t *cur, const int32_t *want, int32_t *free_pages,
+                                const int32_t *n_free, int32_t *n_free_out, int32_t *table, int32_t *cu,
+                                int64_t *slot, unsigned *status, cudaStream_t st) {
+    const size_t smem = 3 * (size_t)(s.B + 1) * sizeof(int);
+    if (smem > 40 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    // every CTA repeats the scan, so one per 2,048 slots or sequences is enough
+    const long long work = max((long long)s.tokens, (long long)s.B);
+    const unsigned grid = (unsigned)max(1ll, min((work + 2047) / 2048, (long long)max(1, sm_count())));
+    paged_tables_kernel<<<grid, kTabThreads, smem, st>>>(s, cur, want, free_pages, n_free, n_free_out, table, cu,
+                                                         slot, status);
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const PagedShape &s, const void *K, const void *V, long long ts, long long hs,
+                                const int64_t *slot, const int32_t *cu, const int32_t *nl, uint8_t *K8, uint8_t *V8,
+                                float *ks, float *vs, void *L, unsigned *status, cudaStream_t st) {
+    if (s.tokens == 0) return cudaSuccess;
+    auto f = s.dtype == SA_BF16 ? (s.code == SA_E4M3 ? append_t<__nv_bfloat16, SA_E4M3> : append_t<__nv_bfloat16, SA_INT8>)
+                                : (s.code == SA_E4M3 ? append_t<float, SA_E4M3> : append_t<float, SA_INT8>);
+    return f(s, K, V, ts, hs, slot, cu, nl, K8, V8, ks, vs, L, status, st);
+}
+
+cudaError_t launch_paged_gather(const PagedShape &s, const int64_t *slot, const uint8_t *K8, const uint8_t *V8,
+                                const float *ks, const float *vs, void *K, void *V, long long ts, long long hs,
+                                unsigned *status, cudaStream_t st) {
+    if (s.tokens == 0) return cudaSuccess;
+    auto f = s.dtype == SA_BF16 ? (s.code == SA_E4M3 ? gather_t<__nv_bfloat16, SA_E4M3> : gather_t<__nv_bfloat16, SA_INT8>)
+                                : (s.code == SA_E4M3 ? gather_t<float, SA_E4M3> : gather_t<float, SA_INT8>);
+    return f(s, slot, K8, V8, ks, vs, K, V, ts, hs, status, st);
+}
+
+}  // namespace sa

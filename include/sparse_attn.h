@@ -27,7 +27,8 @@
  * Groups of entry points: the path (landmarks, selection, prefill, decode),
  * ragged decode batches and landmark refresh, the backward of the gated
  * prefill (sparse_attn_prefill_backward, sparse_attn_select_backward), the
- * flat clustered index (sparse_attn_lsa_*), a decode that allocates nothing
+ * flat clustered index (sparse_attn_lsa_*), a paged key/value cache in 8 bits
+ * (sparse_attn_paged_*), a decode that allocates nothing
  * (sparse_attn_decode_static), and helpers (workspace sizes, status word,
  * error strings, counters).
  *
@@ -410,12 +411,136 @@ int sparse_attn_lsa_tree_decode(const sa_lsa_params *p, int fanout, int beam, co
                                 const void *tree, void *o, float *lse, int32_t *kept, int32_t *compared, void *ws,
                                 size_t ws_bytes, void *stream);
 
+/* ---- Paged 8-bit key/value cache -----------------------------------------
+ * The cache of many sequences in pages: a page holds `block` tokens of every
+ * kv-head (one selection block), so the lists of
+ * sparse_attn_select_decode_varlen address it as they are.
+ *   K8, V8   codes  [pages, Hkv, block, d], one byte each
+ *   kscale,  fp32   [pages, Hkv]; a cached value is code * scale.  Any finite
+ *   vscale          scales >= 0 can be read; those that append writes are
+ *                   powers of two
+ *   table    int32  [B, max_blocks]: page of each block of each sequence;
+ *                   entries behind a sequence's last block are never read
+ *   lengths  int32  [B]: tokens of each sequence, 0 .. max_blocks * block
+ *                   (0: an empty row of the batch)
+ * Packed per-token tensors hold the new tokens of sequence 0, then those of
+ * sequence 1, ...: rows cu[b] .. cu[b + 1] - 1 belong to sequence b, cu int32
+ * [B + 1].  They have `tokens` rows; rows from cu[B] on are padding, which no
+ * call reads or writes unless stated.  Codes are e4m3 (every bit pattern is a
+ * number: the two NaN patterns, which append never writes, read as +-480) or
+ * int8.  A page belongs to one sequence as far as the calls below write to it;
+ * the attention may read shared ones.  Status bits as for
+ * sparse_attn_check_status, and 16: pages or slots ran out. */
+typedef struct {
+    int B;          /* sequences, 1 .. 16384                                        */
+    int Hq, Hkv;    /* query and key/value heads; Hq % Hkv == 0                     */
+    int d;          /* head dim: 64 or 128                                          */
+    int block;      /* tokens per page: 16 .. 128, a multiple of 16                 */
+    int pages;      /* pages of the cache; pages * Hkv * block < 2^31               */
+    int max_blocks; /* columns of the block table                                   */
+    int tokens;     /* rows of the packed per-token tensors, >= 0                   */
+    int top_k;      /* decode with lists: their budget, 0 .. 256                    */
+    int flags;      /* SA_* flags                                                   */
+    int dtype;      /* SA_BF16 or SA_FP32: type of q, K, V, O and the landmarks     */
+    int code;       /* SA_E4M3 or SA_INT8: type of the cached codes                 */
+    float scale;    /* logit scale; 0 selects 1/sqrt(d)                             */
+} sa_paged_params;
+
+/* code types */
+enum { SA_E4M3 = 0, SA_INT8 = 1 };
+
+/* operations, for sparse_attn_paged_workspace_size */
+enum { SA_OP_PAGED_TABLES = 0, SA_OP_PAGED_APPEND = 1, SA_OP_PAGED_GATHER = 2, SA_OP_PAGED_DECODE = 3,
+       SA_OP_PAGED_PREFILL = 4 };
+
+/* Bytes of workspace `op` needs (0: invalid parameters).  Rules as for
+ * sparse_attn_workspace_size: zero-filled once when allocated, calls that
+ * share one must not overlap on the GPU, and one that reported a device-side
+ * timeout is zero-filled again.  Sized by B, Hq, Hkv, d, flags and tokens: a
+ * workspace serves every parameter set that needs no more than it holds and
+ * has the same B, Hq, Hkv and flags. */
+size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op);
+
+/* Block tables and slot maps of one step: sequence b goes from cur_len[b] to
+ * new_len[b] tokens.  A sequence that shrinks (new_len 0: it ends) gives the
+ * pages behind its new last block back to the free stack, in order of
+ * (sequence, block); one that grows takes the pages it lacks from the top of
+ * the stack, in the same order, after every release.
+ *   free_pages int32 [pages]  the stack, n_free[0] entries from the bottom
+ *   n_free -> n_free_out      entries before and after (int32 [1]; they must
+ *                             not be the same word, so that a call can be
+ *                             repeated on the same inputs)
+ *   table                     new entries are written, the others left
+ *   cu int32 [B + 1]          offsets of each sequence's new tokens
+ *   slot int64 [tokens]       page * block + row of each new token; -1 for
+ *                             the rows behind the last one
+ * When the pages or the `tokens` slots do not suffice (status bit 16), or a
+ * length or n_free is out of range (bit 1), nothing is given or taken:
+ * n_free_out = n_free, cu = 0, every slot -1. */
+int sparse_attn_paged_tables(const sa_paged_params *p, const int32_t *cur_len, const int32_t *new_len,
+                             int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int32_t *table,
+                             int32_t *cu, int64_t *slot, void *ws, size_t ws_bytes, void *stream);
+
+/* Quantises new keys and values into the cache.  K, V: row i, head h at
+ * i * tok_stride + h * head_stride elements (0, 0: dense [tokens, Hkv, d]; a
+ * slice of a fused projection or [Hkv, N, d] work too; strides of whole 16
+ * bytes).  slot as from sparse_attn_paged_tables; negative: the row is
+ * skipped.  The slots that one call writes of one page must be consecutive,
+ * ascending and adjacent in `slot` (each slot once), and the rows of the page
+ * before the first of them are the tokens it already holds.  Per (page, head),
+ * with M = 448 (e4m3) or 127 (int8) and amax the largest finite magnitude of
+ * the new rows: the scale is kept when the page holds tokens and amax <= M *
+ * scale, else it becomes the smallest power of two s >= 2^-126 with amax <=
+ * M s, and codes already there are rounded again, code * old / s.  code =
+ * value / s rounded to nearest even; NaN is stored as 0 and infinities as the
+ * largest code, both with status bit 2.
+ * L (may be NULL): landmarks [B, Hkv, max_blocks, d] of the touched blocks,
+ * the mean of their cached keys; needs cu and new_len as given to and from
+ * sparse_attn_paged_tables (row i of sequence b is its position new_len[b] -
+ * cu[b + 1] + i; a slot elsewhere in its block sets status bit 1 and leaves
+ * the landmark). */
+int sparse_attn_paged_append(const sa_paged_params *p, const void *K, const void *V, long long tok_stride,
+                             long long head_stride, const int64_t *slot, const int32_t *cu, const int32_t *new_len,
+                             void *K8, void *V8, float *kscale, float *vscale, void *L, void *ws, size_t ws_bytes,
+                             void *stream);
+
+/* Reads cached rows back: row i of K and V (strides as for append, rows must
+ * not overlap) = the cached key and value at slot[i], rounded to dtype; zeros
+ * where slot[i] is negative (padding included). */
+int sparse_attn_paged_gather(const sa_paged_params *p, const int64_t *slot, const void *K8, const void *V8,
+                             const float *kscale, const float *vscale, void *K, void *V, long long tok_stride,
+                             long long head_stride, void *ws, size_t ws_bytes, void *stream);
+
+/* Decode over the cache: one query per sequence, at position seq_len[b] - 1,
+ * q [B, Hq, d] -> o [B, Hq, d], lse [B, Hq].  With lists (idx, score, count as
+ * from sparse_attn_select_decode_varlen with N = max_blocks * block): the kept
+ * blocks, gated, hierarchical or plain as in sparse_attn_decode_varlen.
+ * Without (idx, score and count NULL): every block of the sequence; SA_GATE
+ * and SA_HIER are SA_ERR_UNSUPPORTED then.  A sequence of length 0 or without
+ * a block gives o = 0, lse = -inf. */
+int sparse_attn_paged_decode(const sa_paged_params *p, const void *q, const void *K8, const void *V8,
+                             const float *kscale, const float *vscale, const int32_t *table, const int32_t *seq_len,
+                             const int32_t *idx, const float *score, const int32_t *count, void *o, float *lse,
+                             void *ws, size_t ws_bytes, void *stream);
+
+/* Packed chunks of queries over the cache: row cu[b] + t of Q [tokens, Hq, d]
+ * is query t of sequence b's T = cu[b + 1] - cu[b].  With SA_CAUSAL it sits at
+ * position seq_len[b] - T + t and sees the keys up to its own (a chunk of a
+ * prompt, drafted tokens); without, it sees all seq_len[b] keys (cross
+ * attention to states of another length).  Every block is read: SA_GATE and
+ * SA_HIER are SA_ERR_UNSUPPORTED.  O [tokens, Hq, d], lse [tokens, Hq]; a row
+ * that sees no key gives O = 0, lse = -inf; rows from cu[B] on are left. */
+int sparse_attn_paged_prefill(const sa_paged_params *p, const void *Q, const int32_t *cu, const void *K8,
+                              const void *V8, const float *kscale, const float *vscale, const int32_t *table,
+                              const int32_t *seq_len, void *O, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronises `stream`, returns SA_OK or SA_ERR_DEVICE from the status
  * word in `ws`, and clears it.  *detail (may be NULL) receives the raw bits:
  * 1 index list entry out of range, 2 NaN score, 4 bounded wait expired, 8 a
  * gather whose first row lies outside the slab it means to read (only in the
  * address-checking build, libsparse_attn_bounds.so, compiled with
- * -DSA_DEBUG_BOUNDS; the release build makes no such check). */
+ * -DSA_DEBUG_BOUNDS; the release build makes no such check), 16 pages or slots
+ * ran out (sparse_attn_paged_tables). */
 int sparse_attn_check_status(void *ws, void *stream, int *detail);
 
 /* Static string for a return code. */
