@@ -27,22 +27,30 @@ __device__ __forceinline__ int paged_len(const PagedShape &s, const int32_t *seq
     return min(max(seq_len[b], 0), s.maxb * s.bs);
 }
 
-// An e4m3 code as fp32.  Moving sign and the seven value bits into an fp16
-// gives the value / 256 exactly, subnormal codes included; the two NaN codes,
-// which the append never writes, read as +-480.
-__device__ __forceinline__ float e4m3_value(unsigned c) {
-    const unsigned short h = (unsigned short)(((c & 0x80u) << 8) | ((c & 0x7fu) << 7));
-    return __half2float(__ushort_as_half(h)) * 256.f;
+// Four codes of one word as fp32, in byte order (exact; the NaN patterns of
+// e4m3, which the append never writes, are NaN).
+template <int kCode>
+__device__ __forceinline__ void code_values4(uint32_t w, float *f) {
+    if (kCode == SA_E4M3) {
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
+        f[0] = a.x;
+        f[1] = a.y;
+        f[2] = b.x;
+        f[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = (float)(signed char)((w >> (8 * i)) & 0xffu);
+    }
 }
 template <int kCode>
 __device__ __forceinline__ float code_value(unsigned byte) {
-    return kCode == SA_E4M3 ? e4m3_value(byte) : (float)(signed char)byte;
-}
-// Four codes of one word, in byte order.
-template <int kCode>
-__device__ __forceinline__ void code_values4(uint32_t w, float *f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = code_value<kCode>((w >> (8 * i)) & 0xffu);
+    float f[4];
+    code_values4<kCode>(byte, f);
+    return f[0];
 }
 // Two finite values rounded to codes (nearest, ties to even; saturating), the
 // first in the low byte.
@@ -58,14 +66,6 @@ __device__ __forceinline__ uint32_t codes_of2(float a, float b) {
     return (uint32_t)(x & 0xff) | ((uint32_t)(y & 0xff) << 8);
 }
 
-// Workspace of the paged calls: the status word, the decode's completion
-// counters (one per unit and group of 16 heads; zero between calls), then
-// scratch that every call reuses.
-struct PagedWs {
-    size_t cnt;       // decode: [B * Hsel * head groups]
-    size_t scratch;
-};
-PagedWs paged_ws(const PagedShape &s);
 
 cudaError_t launch_paged_tables(const PagedShape &s, const int32_t *cur, const int32_t *want, int32_t *free_pages,
                                 const int32_t *n_free, int32_t *n_free_out, int32_t *table, int32_t *cu,
@@ -94,5 +94,11 @@ struct PagedLists {
 // One query per sequence (cu null), or packed chunk rows (cu given, no lists).
 cudaError_t launch_paged_simt(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
                               const PagedLists &l, void *o, float *lse, unsigned *status, cudaStream_t st);
+
+// The tensor-core decode: bf16, `scratch` of paged_decode_scratch bytes.
+bool paged_decode_supported(const PagedShape &s);
+size_t paged_decode_scratch(const PagedShape &s);
+cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
+                                float *lse, unsigned *status, void *scratch, cudaStream_t st);
 
 }  // namespace sa

@@ -70,13 +70,6 @@ int resolve_strides(const PagedShape &s, long long &ts, long long &hs) {
 
 }  // namespace
 
-PagedWs sa::paged_ws(const PagedShape &s) {
-    PagedWs w;
-    w.cnt = kStatusBytes;
-    w.scratch = w.cnt + al256((size_t)s.B * s.Hsel * ((s.heads_per + 15) / 16) * 4);
-    return w;
-}
-
 extern "C" {
 
 size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op) {
@@ -86,8 +79,8 @@ size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op) {
         case SA_OP_PAGED_TABLES:
         case SA_OP_PAGED_APPEND:
         case SA_OP_PAGED_GATHER: return kStatusBytes;
-        case SA_OP_PAGED_DECODE:
-        case SA_OP_PAGED_PREFILL: return paged_ws(s).scratch;
+        case SA_OP_PAGED_DECODE: return kStatusBytes + al256(paged_decode_scratch(s));
+        case SA_OP_PAGED_PREFILL: return kStatusBytes;
         default: return 0;
     }
 }
@@ -156,6 +149,9 @@ int sparse_attn_paged_decode(const sa_paged_params *p, const void *q, const void
     if (ws_bytes < sparse_attn_paged_workspace_size(p, SA_OP_PAGED_DECODE)) return SA_ERR_WORKSPACE;
     const PagedCache c{(const uint8_t *)K8, (const uint8_t *)V8, kscale, vscale, table, seq_len};
     const PagedLists l{idx, score, count};
+    if (paged_decode_supported(s))
+        return launch_result(launch_paged_decode(s, q, c, l, o, lse, (unsigned *)ws,
+                                                 (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
     return launch_result(launch_paged_simt(s, q, nullptr, c, l, o, lse, (unsigned *)ws, (cudaStream_t)stream));
 }
 

@@ -1,0 +1,806 @@
+// paged_decode.cu -- decode over the paged 8-bit cache for bf16 queries: one
+// pass over the kept pages, warp-level tensor-core tiles.
+//
+//   z = scale ks <q, code_k> + gate,   o = sum p vs code_v / sum p,
+//   p = 2^(z log2 e - m)
+//
+// HBM bound: 2 d bytes a key and kv-head, 4 G flops a byte.  So everything is
+// built to keep loads in flight and to spend few instructions per byte:
+//   * the work is one line of stages (up to 64 keys of one unit: a page, half
+//     a page of more than 64 tokens, or several small pages), units one after
+//     the other, cut into equal ranges, one per warp of the grid whatever the
+//     lengths or lists are.  A warp streams its range by itself: it issues the
+//     TMA loads of its own ring, waits for them and computes; no warp waits
+//     for another.  A unit that lies in one range is finished by its warp; the
+//     others leave a record (max, sum, acc) per range, at most two a warp,
+//     which a second launch joins in range order;
+//   * codes become fp16 in registers (exact), so the tensor core multiplies
+//     them as they are, and scales stay out of the matrices: a key's scale
+//     multiplies its logits, a value's the finished product of its page;
+//   * keys are the M side of both products (S^T = K q^T, O^T = V^T P^T): a
+//     tile holds 16 keys x 8 query heads, so a group of 4 to 8 heads wastes
+//     little, and P^T comes out of S^T by a register transpose (movmatrix);
+//   * a matrix row of a tile is any key or dimension as long as both operands
+//     agree, so the byte order that ldmatrix gives is used as it is: for S the
+//     query is loaded in that order, for O the even and odd dimensions of 16
+//     form rows 0-7 and 8-15.
+// fp16 queries: each row is scaled by a power of two so that its largest
+// element lies in [2^14, 2^15); what falls below fp16's range is under 2^-38
+// of the largest.  P is rounded to fp16 (2^-11 of each weight; the reference
+// max is raised only when a logit passes it by 2^8, so p stays below 2^8).
+#include <cuda.h>
+#include <math_constants.h>
+
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace sa {
+namespace {
+
+using namespace tc;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 6;      // ranges per CTA
+constexpr int kRing = 2;       // stages per warp
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMinRange = 4;   // stages: shorter ranges cost more in records than they save
+constexpr int kMergeWarps = 8;
+// stage flags: first / last stage of its unit in this range, the unit lies in
+// this range as a whole, it begins before this range, some keys are not there
+enum { F_NEW = 1, F_LAST = 2, F_WHOLE = 4, F_CUT = 8, F_TAIL = 16 };
+
+struct DecArgs {
+    PagedShape s;
+    PagedCache c;
+    PagedLists l;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *o;
+    float *lse;
+    unsigned *status;
+    int2 *info;          // [units] first range, ranges (0: nothing to join)
+    float *rec;          // [ranges][2] records
+    int units, hg;       // units = B * Hsel * hg; hg head groups per list
+    int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
+    int tiles;           // 16-key tiles per stage
+};
+
+// One ring stage's record for its consumer.
+struct __align__(16) Meta {
+    float4 tile[4];      // per 16 keys: key scale, value scale, gate (or score), valid keys
+    int unit, flags, pad[2];
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Four codes to two fp16 pairs, exactly.  kEven: bytes (0, 2) and (1, 3), else
+// (0, 1) and (2, 3).
+template <int kCode, bool kEven>
+__device__ __forceinline__ void to_h2(uint32_t x, uint32_t &p, uint32_t &q) {
+    if (kCode == SA_E4M3) {
+        if (kEven) x = __byte_perm(x, 0, 0x3120);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(p), "=r"(q) : "r"(x));
+    } else {
+        // 1024 + (code + 128) under fp16's exponent of 2^10, then minus 1152
+        x ^= 0x80808080u;
+        uint32_t a = __byte_perm(x, 0x64646464u, kEven ? 0x4240 : 0x4140);
+        uint32_t b = __byte_perm(x, 0x64646464u, kEven ? 0x4341 : 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));
+        __half2 ha = __hsub2(*reinterpret_cast<__half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+        p = *reinterpret_cast<uint32_t *>(&ha);
+        q = *reinterpret_cast<uint32_t *>(&hb);
+    }
+}
+// Byte offset of 16-byte chunk c of row r: the swizzle of the TMA box (128-
+// byte rows: chunk ^ row % 8; 64-byte rows: chunk ^ row / 2 % 4).
+template <int kD>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    return kD == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Where a unit lies: its list, batch and heads.
+struct UnitAt {
+    int b, g, h0, hn;      // heads h0 .. h0 + hn - 1
+    size_t lu;             // list row
+};
+template <int kNT>
+__device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int u) {
+    const PagedShape &s = a.s;
+    UnitAt w;
+    const int grp = u % a.hg;
+    const int lu = u / a.hg, hs = lu % s.Hsel;
+    w.b = lu / s.Hsel;
+    w.lu = (size_t)lu;
+    const bool perq = s.flags & SA_SELECT_PER_QHEAD;
+    w.g = perq ? hs / s.G : hs;
+    w.h0 = (perq ? hs : hs * s.G) + grp * 16;
+    w.hn = min(8 * kNT, s.heads_per - grp * 16);
+    return w;
+}
+
+// Entries (blocks) of a unit: its list's, or every block of its sequence.
+__device__ __forceinline__ int entries_of(const DecArgs &a, int u) {
+    const int lu = u / a.hg, n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
+    if (!a.l.idx) return (n + a.s.bs - 1) / a.s.bs;
+    return n > 0 ? max(0, min(a.l.count[lu], a.s.cap)) : 0;
+}
+__device__ __forceinline__ int stages_of(const DecArgs &a, int entries) {
+    return (entries * a.sub + a.pps - 1) / a.pps;
+}
+
+template <int kD, int kNT>
+constexpr int rec_floats() { return (kD / 16 * kNT * 4 + 4 * kNT) * 32; }
+
+// Softmax state of one warp: heads 8 nt + 2 tq + {0, 1} per lane, dimensions
+// 16 t + 2 gq + {0, 1}.
+template <int kD, int kNT>
+struct Acc {
+    float m[2 * kNT], l[2 * kNT];
+    float o[kD / 16][kNT][4];     // [][][e]: dimension 16 t + 2 gq + (e >> 1), head 8 nt + 2 tq + (e & 1)
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int i = 0; i < 2 * kNT; ++i) {
+            m[i] = -CUDART_INF_F;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+    }
+    __device__ __forceinline__ void scale(const float *f) {
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][n][e] *= f[2 * n + (e & 1)];
+    }
+    __device__ __forceinline__ void save(float *r, int lane) const {
+        int i = 0;
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[32 * i++ + lane] = o[t][n][e];
+#pragma unroll
+        for (int k = 0; k < 2 * kNT; ++k) {
+            r[32 * i++ + lane] = m[k];
+            r[32 * i++ + lane] = l[k];
+        }
+    }
+    // joins a saved record (same lane layout)
+    __device__ __forceinline__ void join(const float *r, int lane) {
+        constexpr int no = kD / 16 * kNT * 4;
+        float x[no];
+#pragma unroll
+        for (int i = 0; i < no; ++i) x[i] = r[32 * i + lane];
+        float fa[2 * kNT], fb[2 * kNT];
+#pragma unroll
+        for (int k = 0; k < 2 * kNT; ++k) {
+            const float m2 = r[32 * (no + 2 * k) + lane], l2 = r[32 * (no + 2 * k + 1) + lane];
+            const float M = fmaxf(m[k], m2);
+            fa[k] = m[k] == -CUDART_INF_F ? 0.f : ex2(m[k] - M);
+            fb[k] = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - M);
+            l[k] = l[k] * fa[k] + l2 * fb[k];
+            m[k] = M;
+        }
+        int i = 0;
+#pragma unroll
+        for (int t = 0; t < kD / 16; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e, ++i)
+                    o[t][n][e] = o[t][n][e] * fa[2 * n + (e & 1)] + x[i] * fb[2 * n + (e & 1)];
+    }
+    __device__ __forceinline__ void store(const DecArgs &a, const UnitAt &w, int lane) const {
+        const int gq = lane >> 2, tq = lane & 3;
+#pragma unroll
+        for (int k = 0; k < 2 * kNT; ++k) {
+            const int h = 8 * (k >> 1) + 2 * tq + (k & 1);
+            if (h >= w.hn) continue;
+            const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
+            const size_t row = (size_t)w.b * a.s.Hq + w.h0 + h;
+            __nv_bfloat16 *dst = a.o + row * kD + 2 * gq;
+#pragma unroll
+            for (int t = 0; t < kD / 16; ++t)
+                *reinterpret_cast<__nv_bfloat162 *>(dst + 16 * t) = __floats2bfloat162_rn(
+                    l[k] == 0.f ? 0.f : o[t][k >> 1][k & 1] * inv, l[k] == 0.f ? 0.f : o[t][k >> 1][2 + (k & 1)] * inv);
+            if (gq == 0) a.lse[row] = l[k] == 0.f ? -CUDART_INF_F : (m[k] + log2f(l[k])) * kLn2;
+        }
+    }
+};
+
+// What a warp knows of the stages it issues next: up to 32 parts of one unit,
+// one per lane, loaded in steps so that the chain count -> list -> table ->
+// scales is in flight behind the stages before it.
+struct Batch {
+    int unit, entries;          // -1: none
+    int s0, s1;                 // stages of the unit
+    int flags;                  // F_NEW: s0 is the unit's first stage here; F_LAST: s1 - 1 its last; F_WHOLE, F_CUT
+    int step;                   // load steps done
+    int blk, page, nk;          // lane: block (-1: none), page, valid keys of its part
+    float ks, vs, gate;
+};
+
+template <int kD, int kCode, int kNT>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecArgs a) {
+    constexpr uint32_t kHalfBytes = 64 * kD;
+    extern __shared__ unsigned char dec_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dec_raw) + 1023) &
+                                                          ~uintptr_t(1023));
+    __shared__ Meta meta[kWarps][kRing];
+    __shared__ uint64_t bars[kWarps][kRing];
+    __shared__ long long pre[kThreads + 1];
+    __shared__ long long wtot[kWarps];
+    __shared__ volatile int abort_s;
+    const PagedShape &s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+    const bool hier = s.flags & SA_HIER;
+    if (tid == 0) {
+        for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+        abort_s = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- the line of stages: offsets of each thread's share of the units -----
+    const int share = (a.units + kThreads - 1) / kThreads;
+    {
+        const int u0 = min(a.units, tid * share), u1 = min(a.units, u0 + share);
+        long long n = 0;
+        for (int u = u0; u < u1; ++u) {
+            const int e = entries_of(a, u);
+            n += stages_of(a, e);
+            if (e == 0 && u % gridDim.x == blockIdx.x) {
+                // nothing kept: zeros
+                const UnitAt w = unit_at<kNT>(a, u);
+                a.info[u] = make_int2(0, 0);
+                for (int h = 0; h < w.hn; ++h) {
+                    const size_t row = (size_t)w.b * s.Hq + w.h0 + h;
+                    for (int i = 0; i < kD; i += 8)
+                        *reinterpret_cast<uint4 *>(a.o + row * kD + i) = make_uint4(0, 0, 0, 0);
+                    a.lse[row] = -CUDART_INF_F;
+                }
+            }
+        }
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) wtot[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) inc += wtot[w];
+        pre[tid] = inc - n;
+        if (tid == kThreads - 1) pre[kThreads] = inc;
+        __syncthreads();
+    }
+    const long long total = pre[kThreads];
+    const int ranges = gridDim.x * kWarps;
+    const long long per = max((long long)kMinRange, (total + ranges - 1) / ranges);
+    // neighbouring ranges go to different SMs, so that a small call spreads out
+    const int range = warp * gridDim.x + blockIdx.x;
+    const long long x0 = range * per, x1 = min(total, x0 + per);
+    if (x0 >= x1) return;
+
+    // ---- issue side ----------------------------------------------------------
+    int bu;                            // unit of stage xi, and its first stage
+    long long bpu, xi = x0;            // xi: next stage to put in a batch
+    {
+        int best = 0;
+        for (int t = lane; t < kThreads; t += 32)
+            if (pre[t] <= x0) best = t;
+        best = __reduce_max_sync(~0u, best);
+        bu = best * share;
+        bpu = pre[best];
+    }
+    // step 0: unit and part of the line
+    auto open = [&](Batch &t) {
+        t.step = 0;
+        t.unit = -1;
+        if (xi >= x1) return;
+        int n;
+        for (;;) {
+            t.entries = entries_of(a, bu);
+            n = stages_of(a, t.entries);
+            if (xi < bpu + n) break;
+            bpu += n;
+            ++bu;
+        }
+        t.unit = bu;
+        t.s0 = (int)(xi - bpu);
+        t.s1 = (int)min((long long)min(n, t.s0 + 32 / a.pps), x1 - bpu);
+        t.flags = (t.s0 == 0 || xi == x0 ? F_NEW : 0) | (t.s1 == n || bpu + t.s1 == x1 ? F_LAST : 0) |
+                  (bpu < x0 ? F_CUT : 0) | (bpu >= x0 && bpu + n <= x1 ? F_WHOLE : 0);
+        if (t.s0 == 0 && lane == 0) {
+            // how many ranges the unit's first one shares it with
+            const int r1 = (int)((bpu + n - 1) / per);
+            a.info[bu] = r1 == range ? make_int2(0, 0) : make_int2(range, r1 - range + 1);
+        }
+        xi = bpu + t.s1;
+        t.step = 1;
+    };
+    // steps 1 to 3, one dependent load each
+    auto more = [&](Batch &t) {
+        const UnitAt w = unit_at<kNT>(a, t.unit);
+        if (t.step == 1) {
+            const int c = t.s0 * a.pps + lane, e = c / a.sub;
+            t.blk = -1;
+            t.gate = 0.f;
+            t.nk = 0;
+            if (lane < (t.s1 - t.s0) * a.pps && e < t.entries) {
+                const int n = paged_len(s, a.c.seq_len, w.b), local = (n + s.bs - 1) / s.bs - 1;
+                t.blk = e;
+                if (a.l.idx) {
+                    const int32_t *il = a.l.idx + w.lu * s.cap;
+                    const float *sc = a.l.score + w.lu * s.cap;
+                    const int before = e > 0 ? il[e - 1] : -1;
+                    const float mine = sc[e], loc = sc[t.entries - 1];
+                    t.blk = il[e];
+                    if (t.blk <= before || t.blk < 0 || t.blk > local) {
+                        set_status(a.status, kStatusBadIndex);
+                        t.blk = -1;
+                    }
+                    const bool forced = (t.blk == local && (s.flags & SA_LOCAL)) || (t.blk == 0 && (s.flags & SA_SINK));
+                    t.gate = hier ? mine * kLog2e
+                                  : ((s.flags & SA_GATE) && !forced ? log_sigmoid(mine - loc) * kLog2e : 0.f);
+                }
+                const int row0 = (c - e * a.sub) * a.rows;
+                t.nk = min(min(a.rows, s.bs - row0), n - t.blk * s.bs - row0);
+                if (t.nk <= 0) t.blk = -1;
+            }
+        } else if (t.step == 2) {
+            t.page = t.blk >= 0 ? a.c.table[(size_t)w.b * s.maxb + t.blk] : -1;
+        } else {
+            if (t.blk >= 0 && (t.page < 0 || t.page >= s.pages)) {
+                set_status(a.status, kStatusBadIndex);
+                t.page = -1;
+            }
+            t.ks = t.vs = 0.f;
+            if (t.page >= 0) {
+                const size_t ph = (size_t)t.page * s.Hkv + w.g;
+                t.ks = a.c.ks[ph];
+                t.vs = a.c.vs[ph];
+            }
+        }
+        ++t.step;
+    };
+    Batch cur, nxt;
+    open(cur);
+    while (cur.step < 4) more(cur);
+    open(nxt);
+    int ci = 0;                        // stages of cur already issued
+    const uint32_t ring = smem_u32(sm) + warp * kRing * 2 * kHalfBytes;
+    const uint32_t bar0 = smem_u32(&bars[warp][0]);
+    const uint32_t part_bytes = (uint32_t)a.rows * kD;
+    // loads the range's next stage into `slot`; false when there is none
+    auto issue = [&](int slot) -> bool {
+        if (cur.unit >= 0 && ci == cur.s1 - cur.s0) {
+            while (nxt.unit >= 0 && nxt.step < 4) more(nxt);
+            cur = nxt;
+            ci = 0;
+            open(nxt);
+        }
+        if (cur.unit < 0) return false;
+        Meta &md = meta[warp][slot];
+        const int part = lane - ci * a.pps;
+        const bool mine = part >= 0 && part < a.pps, live = mine && cur.page >= 0;
+        const unsigned lives = __ballot_sync(~0u, live);
+        const bool tail = __any_sync(~0u, mine && (!live || cur.nk < a.rows));
+        if (mine) {
+            const int t16 = a.rows >> 4;
+            for (int t = 0; t < t16; ++t)
+                md.tile[part * t16 + t] = make_float4(cur.ks, cur.vs, cur.gate,
+                                                      __int_as_float(live ? max(0, min(16, cur.nk - 16 * t)) : 0));
+        }
+        const uint32_t bar = bar0 + 8 * slot;
+        if (lane == 0) {
+            md.unit = cur.unit;
+            md.flags = (cur.flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cur.flags & F_NEW : 0) |
+                       (ci == cur.s1 - cur.s0 - 1 ? cur.flags & F_LAST : 0) | (tail ? F_TAIL : 0);
+            if (lives) mbar_expect_tx(bar, 2 * part_bytes * __popc(lives));
+            else mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (live) {
+            const int row0 = ((cur.s0 * a.pps + lane) % a.sub) * a.rows;
+            const int g = unit_at<kNT>(a, cur.unit).g;
+            const int y = (cur.page * s.Hkv + g) * s.bs + row0;
+            const uint32_t dst = ring + slot * 2 * kHalfBytes + part * part_bytes;
+            tma_load_2d(dst, &tmK, bar, 0, y);
+            tma_load_2d(dst + kHalfBytes, &tmV, bar, 0, y);
+        }
+        ++ci;
+        if (nxt.unit >= 0 && nxt.step < 4) more(nxt);
+        return true;
+    };
+
+    // ---- consumer side -------------------------------------------------------
+    Acc<kD, kNT> acc;
+    uint32_t qb[kD / 16][kNT][2];
+    float qf[2 * kNT];
+    int issued = 0, done = 0;
+    for (; issued < kRing; ++issued)
+        if (!issue(issued)) break;
+    bool ok = true;
+    for (; done < issued; ++done) {
+        const int slot = done % kRing;
+        ok = mbar_wait(bar0 + 8 * slot, (done / kRing) & 1, &abort_s, a.status);
+        if (!__all_sync(~0u, ok)) break;
+        const Meta &md = meta[warp][slot];
+        const int flags = md.flags, unit = md.unit;
+        float4 ti[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            ti[t] = t < a.tiles ? md.tile[t] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (flags & F_NEW) {
+            // the unit's queries: dimensions 16 k + 4 tq + {0, 1}, {2, 3} of head 8 n + gq
+            const UnitAt w = unit_at<kNT>(a, unit);
+            acc.reset();
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+                const int h = 8 * n + gq;
+                const __nv_bfloat16 *src = a.q + ((size_t)w.b * s.Hq + w.h0 + (h < w.hn ? h : 0)) * kD + 4 * tq;
+                uint2 x[kD / 16];
+                unsigned big = 0;      // largest magnitude's bits
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    x[k] = h < w.hn ? *reinterpret_cast<const uint2 *>(src + 16 * k) : make_uint2(0, 0);
+                    const unsigned y = __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
+                    big = __vmaxu2(big, y);
+                }
+                big = max(big & 0xffffu, big >> 16);
+                big = max(big, __shfl_xor_sync(~0u, big, 1));
+                big = max(big, __shfl_xor_sync(~0u, big, 2));
+                // 2^(14 - exponent), within fp32's normal powers
+                const int e = (int)(big >> 7) - 127;
+                const int up = max(-113, min(126, 14 - e));
+                const float f = __uint_as_float((unsigned)(up + 127) << 23);
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    const float2 lo = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x[k].x));
+                    const float2 hi = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x[k].y));
+                    qb[k][n][0] = pack_h2(lo.x * f, lo.y * f);
+                    qb[k][n][1] = pack_h2(hi.x * f, hi.y * f);
+                }
+                // logit factor of the heads this lane's S columns hold
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int up2 = __shfl_sync(~0u, up, (2 * tq + i) * 4);
+                    qf[2 * n + i] = s.scale * kLog2e * __uint_as_float((unsigned)(127 - up2) << 23);
+                }
+            }
+        }
+        const uint32_t kb = ring + slot * 2 * kHalfBytes, vb = kb + kHalfBytes;
+        const int mrow = (lane & 7) + (lane & 8), mch = lane >> 4;   // row and chunk of the lane's ldmatrix address
+        // S^T = K q^T: 16 keys x 8 heads per tile
+        float z[4][kNT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) z[t][n][0] = z[t][n][1] = z[t][n][2] = z[t][n][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (t >= a.tiles) continue;
+                uint32_t r[4], p0, q0, p1, q1;
+                ldsm4(kb + swz<kD>(16 * t + mrow, 2 * k + mch), r);
+                to_h2<kCode, false>(r[0], p0, q0);
+                to_h2<kCode, false>(r[1], p1, q1);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) mma_f16(z[t][n], p0, p1, q0, q1, qb[2 * k][n][0], qb[2 * k][n][1]);
+                to_h2<kCode, false>(r[2], p0, q0);
+                to_h2<kCode, false>(r[3], p1, q1);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                    mma_f16(z[t][n], p0, p1, q0, q1, qb[2 * k + 1][n][0], qb[2 * k + 1][n][1]);
+            }
+        // logits in log2 units, -inf where there is no key
+        float top[2 * kNT];
+#pragma unroll
+        for (int i = 0; i < 2 * kNT; ++i) top[i] = -CUDART_INF_F;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int nk = t < a.tiles ? __float_as_int(ti[t].w) : 0;
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = fmaf(z[t][n][e], qf[2 * n + (e & 1)] * ti[t].x, hier ? 0.f : ti[t].z);
+                    z[t][n][e] = gq + 8 * (e >> 1) < nk ? x : -CUDART_INF_F;
+                    top[2 * n + (e & 1)] = fmaxf(top[2 * n + (e & 1)], z[t][n][e]);
+                }
+        }
+        float pf[2 * kNT];     // hierarchical: weight of the block over its sum
+        if (!hier) {
+            bool high = false;
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i) high |= top[i] > acc.m[i] + 8.f;
+            if (__any_sync(~0u, high)) {
+                float f[2 * kNT];
+#pragma unroll
+                for (int i = 0; i < 2 * kNT; ++i) {
+                    float x = top[i];
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                    x = fmaxf(x, acc.m[i]);
+                    f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - x);
+                    acc.m[i] = x;
+                    acc.l[i] *= f[i];
+                }
+                acc.scale(f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i) {
+                float x = top[i];
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                top[i] = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            }
+        }
+        float sum[2 * kNT];
+#pragma unroll
+        for (int i = 0; i < 2 * kNT; ++i) sum[i] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 2 * n + (e & 1);
+                    const float ref = hier ? top[i] : acc.m[i];
+                    const float p = ex2(z[t][n][e] - (ref == -CUDART_INF_F ? 0.f : ref));
+                    z[t][n][e] = p;
+                    sum[i] += p;
+                }
+        if (hier) {
+            float f[2 * kNT];
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i) {
+                float lb = sum[i];
+                lb += __shfl_xor_sync(~0u, lb, 4);
+                lb += __shfl_xor_sync(~0u, lb, 8);
+                lb += __shfl_xor_sync(~0u, lb, 16);
+                f[i] = 1.f;
+                pf[i] = 0.f;
+                if (lb > 0.f) {
+                    const float M = fmaxf(acc.m[i], ti[0].z);
+                    f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - M);
+                    const float w = ex2(ti[0].z - M);
+                    acc.m[i] = M;
+                    // the sum over lanes at the end counts it once
+                    acc.l[i] = acc.l[i] * f[i] + (gq == 0 ? w : 0.f);
+                    pf[i] = w / lb;
+                }
+            }
+            acc.scale(f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i) acc.l[i] += sum[i];
+        }
+        // P^T as the second operand: keys 16 t + 2 tq + {0, 1} (+ 8), head 8 n + gq
+        uint32_t pb[4][kNT][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+                const float f0 = hier ? pf[2 * n] : 1.f, f1 = hier ? pf[2 * n + 1] : 1.f;
+                pb[t][n][0] = transpose8(pack_h2(z[t][n][0] * f0, z[t][n][1] * f1));
+                pb[t][n][1] = transpose8(pack_h2(z[t][n][2] * f0, z[t][n][3] * f1));
+            }
+        // O^T += V^T P^T, 32 dimensions at a time
+        const bool one_page = a.pps == 1;
+        const bool blank = kCode == SA_E4M3 && (flags & F_TAIL);   // what is not a key may hold NaN codes
+#pragma unroll
+        for (int np = 0; np < kD / 32; ++np) {
+            float d[2][kNT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) d[h][n][0] = d[h][n][1] = d[h][n][2] = d[h][n][3] = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (t >= a.tiles) continue;
+                uint32_t r[4];
+                ldsm4t(vb + swz<kD>(16 * t + mrow, 2 * np + mch), r);
+                if (blank) {
+                    const int nk = __float_as_int(ti[t].w);
+                    const uint32_t m0 = (2 * tq < nk ? 0xffffu : 0u) | (2 * tq + 1 < nk ? 0xffff0000u : 0u);
+                    const uint32_t m1 = (2 * tq + 8 < nk ? 0xffffu : 0u) | (2 * tq + 9 < nk ? 0xffff0000u : 0u);
+                    r[0] &= m0;
+                    r[1] &= m1;
+                    r[2] &= m0;
+                    r[3] &= m1;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a0, a1, a2, a3;
+                    to_h2<kCode, true>(r[2 * h], a0, a1);
+                    to_h2<kCode, true>(r[2 * h + 1], a2, a3);
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) mma_f16(d[h][n], a0, a1, a2, a3, pb[t][n][0], pb[t][n][1]);
+                }
+                if (!one_page) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                acc.o[2 * np + h][n][e] = fmaf(ti[t].y, d[h][n][e], acc.o[2 * np + h][n][e]);
+                                d[h][n][e] = 0.f;
+                            }
+                }
+            }
+            if (one_page) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc.o[2 * np + h][n][e] = fmaf(ti[0].y, d[h][n][e], acc.o[2 * np + h][n][e]);
+            }
+        }
+        __syncwarp();
+        if (issue(slot)) ++issued;
+        if (flags & F_LAST) {
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i) {
+                acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 4);
+                acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 8);
+                acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 16);
+            }
+            if (flags & F_WHOLE) acc.store(a, unit_at<kNT>(a, unit), lane);
+            else acc.save(a.rec + ((size_t)range * 2 + (flags & F_CUT ? 0 : 1)) * rec_floats<kD, kNT>(), lane);
+        }
+    }
+    if (!ok) {
+        // a wait ran out: let the copies in flight land before the CTA exits
+        volatile int never = 0;
+        for (; done < issued; ++done) mbar_wait(bar0 + 8 * (done % kRing), (done / kRing) & 1, &never, a.status);
+    }
+}
+
+// Joins the records of the units that several ranges shared: warp w takes
+// records w, w + kMergeWarps, ..., then the warps' states are joined in order.
+template <int kD, int kNT>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+paged_merge_kernel(DecArgs a) {
+    __shared__ float part[kMergeWarps / 2][rec_floats<kD, kNT>()];
+    const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 in = a.info[u];
+    if (in.y < 2) return;
+    Acc<kD, kNT> acc;
+    acc.reset();
+    for (int i = warp; i < in.y; i += kMergeWarps)
+        acc.join(a.rec + ((size_t)(in.x + i) * 2 + (i == 0 ? 1 : 0)) * rec_floats<kD, kNT>(), lane);
+#pragma unroll
+    for (int n = kMergeWarps / 2; n > 0; n >>= 1) {
+        if (warp >= n && warp < 2 * n) acc.save(part[warp - n], lane);
+        __syncthreads();
+        if (warp < n) acc.join(part[warp], lane);
+        __syncthreads();
+    }
+    if (warp == 0) acc.store(a, unit_at<kNT>(a, u), lane);
+}
+
+// Rows of codes [rows][d], one byte each, read in boxes of box_rows rows.
+bool code_map(CUtensorMap *map, const uint8_t *base, uint64_t rows, int d, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)d, rows};
+    cuuint64_t strides[1] = {(cuuint64_t)d};
+    cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int head_tiles(const PagedShape &s) { return s.heads_per <= 8 ? 1 : 2; }
+int head_groups(const PagedShape &s) { return (s.heads_per + 15) / 16; }
+size_t rec_bytes(const PagedShape &s) { return (size_t)(s.d / 16 * 4 + 4) * head_tiles(s) * 32 * sizeof(float); }
+// The workspace counts the 148 SMs of a B200; the grid follows the device.
+constexpr int kMaxGrid = 148;
+
+template <int kD, int kCode, int kNT>
+cudaError_t run(const DecArgs &a, int grid, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+    constexpr int smem = kWarps * kRing * 2 * 64 * kD + 1024;
+    auto kern = paged_decode_kernel<kD, kCode, kNT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, mk, mv, a);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_merge_kernel<kD, kNT>, dim3((unsigned)a.units), dim3(32 * kMergeWarps), 0, st, a);
+    note_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+// bf16; a hierarchical block's softmax needs the block in one stage.
+bool paged_decode_supported(const PagedShape &s) {
+    return s.dtype == SA_BF16 && !((s.flags & SA_HIER) && s.bs > 64);
+}
+
+size_t paged_decode_scratch(const PagedShape &s) {
+    const size_t units = (size_t)s.B * s.Hsel * head_groups(s);
+    return ((units * sizeof(int2) + 255) & ~(size_t)255) + (size_t)kMaxGrid * kWarps * 2 * rec_bytes(s);
+}
+
+cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
+                                float *lse, unsigned *status, void *scratch, cudaStream_t st) {
+    DecArgs a{};
+    a.s = s;
+    a.c = c;
+    a.l = l;
+    a.q = (const __nv_bfloat16 *)q;
+    a.o = (__nv_bfloat16 *)o;
+    a.lse = lse;
+    a.status = status;
+    a.hg = head_groups(s);
+    a.units = s.B * s.Hsel * a.hg;
+    a.info = (int2 *)scratch;
+    a.rec = (float *)((unsigned char *)scratch + (((size_t)a.units * sizeof(int2) + 255) & ~(size_t)255));
+    // a page of up to 64 tokens is one part, a longer one two; small pages
+    // share a stage (not in hierarchical mode, where a stage is one block)
+    a.sub = s.bs > 64 ? 2 : 1;
+    a.rows = s.bs > 64 ? (s.bs + 31) / 32 * 16 : s.bs;
+    a.pps = (s.flags & SA_HIER) ? 1 : 64 / a.rows;
+    a.tiles = a.rows * a.pps / 16;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorNoDevice;
+    CUtensorMap mk, mv;
+    const uint64_t rows = (uint64_t)s.pages * s.Hkv * s.bs;
+    if (!code_map(&mk, c.K, rows, s.d, a.rows) || !code_map(&mv, c.V, rows, s.d, a.rows))
+        return cudaErrorInvalidValue;
+    const int grid = min(sms, kMaxGrid);
+    const int key = (s.d == 128 ? 4 : 0) | (s.code == SA_E4M3 ? 2 : 0) | (head_tiles(s) == 2 ? 1 : 0);
+    switch (key) {
+        case 0: return run<64, SA_INT8, 1>(a, grid, mk, mv, st);
+        case 1: return run<64, SA_INT8, 2>(a, grid, mk, mv, st);
+        case 2: return run<64, SA_E4M3, 1>(a, grid, mk, mv, st);
+        case 3: return run<64, SA_E4M3, 2>(a, grid, mk, mv, st);
+        case 4: return run<128, SA_INT8, 1>(a, grid, mk, mv, st);
+        case 5: return run<128, SA_INT8, 2>(a, grid, mk, mv, st);
+        case 6: return run<128, SA_E4M3, 1>(a, grid, mk, mv, st);
+        default: return run<128, SA_E4M3, 2>(a, grid, mk, mv, st);
+    }
+}
+
+}  // namespace sa

@@ -426,9 +426,8 @@ int sparse_attn_lsa_tree_decode(const sa_lsa_params *p, int fanout, int beam, co
  * Packed per-token tensors hold the new tokens of sequence 0, then those of
  * sequence 1, ...: rows cu[b] .. cu[b + 1] - 1 belong to sequence b, cu int32
  * [B + 1].  They have `tokens` rows; rows from cu[B] on are padding, which no
- * call reads or writes unless stated.  Codes are e4m3 (every bit pattern is a
- * number: the two NaN patterns, which append never writes, read as +-480) or
- * int8.  A page belongs to one sequence as far as the calls below write to it;
+ * call reads or writes unless stated.  Codes are e4m3 (append never writes its
+ * NaN patterns) or int8.  A page belongs to one sequence as far as the calls below write to it;
  * the attention may read shared ones.  Status bits as for
  * sparse_attn_check_status, and 16: pages or slots ran out. */
 typedef struct {

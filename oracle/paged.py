@@ -14,12 +14,12 @@ MOST = {E4M3: 448.0, INT8: 127.0}
 
 def e4m3_values() -> np.ndarray:
     """The value of each of the 256 codes: sign, 4 exponent bits (bias 7), 3
-    mantissa bits; exponent 0 is subnormal.  The two NaN patterns read +-480."""
+    mantissa bits; exponent 0 is subnormal; all ones is NaN."""
     out = np.empty(256)
     for c in range(256):
         e, m = (c >> 3) & 15, c & 7
         v = m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)
-        out[c] = -v if c & 128 else v
+        out[c] = np.nan if c & 127 == 127 else -v if c & 128 else v
     return out
 
 
