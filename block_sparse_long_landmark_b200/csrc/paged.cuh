@@ -100,5 +100,10 @@ bool paged_decode_supported(const PagedShape &s);
 size_t paged_decode_scratch(const PagedShape &s);
 cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
                                 float *lse, unsigned *status, void *scratch, cudaStream_t st);
+// The tensor-core chunk attention: bf16, up to 128 query heads per kv-head.
+bool paged_prefill_supported(const PagedShape &s);
+size_t paged_prefill_scratch(const PagedShape &s);
+cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32_t *cu, const PagedCache &c, void *O,
+                                 float *lse, unsigned *status, void *scratch, cudaStream_t st);
 
 }  // namespace sa
