@@ -10,18 +10,23 @@
 // core runs the other's products.  Tensor work 4 rows d flops a key against
 // d conversions a key and d bytes: tensor and exponential bound at 256 rows,
 // cache-read bound when a chunk has few.
-//   * codes reach shared memory as bf16 (exact for e4m3 and int8) through the
-//     registers of a converter warpgroup, which loads one tile ahead straight
-//     from the pages; scales stay out of the matrices: the key's multiplies
-//     the logit, the value's the weight before it is rounded to bf16 (2^-8 of
-//     each weight; bf16 because p vs spans the scales' range);
+//   * TMA brings a tile's codes from its pages to shared memory; a converter
+//     warpgroup makes bf16 keys (as the queries are) and fp16 values of them,
+//     both exactly.  Scales stay out of the matrices: the key's multiplies the
+//     logit, the value's the weight;
+//   * weights are rounded to fp16 (2^-11 of each).  p vs spans the scales'
+//     range, so O has a reference of its own: with m the row's largest logit
+//     and m' its largest logit + log2 vs, l sums p = 2^(z - m) and the tensor
+//     core gets p vs 2^(m - m'), at most 2^8 (references are raised when a
+//     logit passes them by 2^8), whatever the scales;
 //   * the work is one line of (unit, key tile) steps cut into one equal range
 //     per CTA, whatever the lengths: a few queries over a long cache spread
 //     over every SM, and a causal triangle is balanced.  Units that ranges
 //     share leave fp32 records (at most two a CTA), joined by a second launch.
 //
 // Warps: 0 takes segments from the line and loads Q by TMA, 1 owns tensor
-// memory and issues the MMAs, 2-3 idle; 4-7 convert; 8-11 and 12-15 softmax.
+// memory and issues the MMAs, 2 loads codes and scales, 3 idles; 4-7 convert;
+// 8-11 and 12-15 softmax.
 // Registers: launched at 128; 56 + 88 + 2 * 184 = 4 * 128.
 // Every wait is bounded; when one runs out the CTA sets the status word, lets
 // its copies land, frees tensor memory and exits.
@@ -38,7 +43,7 @@ using namespace tc;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 512;
-constexpr int kRegsLaunch = 128, kRegsIssue = 56, kRegsConv = 88, kRegsSoft = 184;
+constexpr int kRegsLaunch = 128, kRegsIssue = 48, kRegsConv = 64, kRegsSoft = 200;
 static_assert(128 * (kRegsIssue + kRegsConv + 2 * kRegsSoft) <= kThreads * kRegsLaunch, "register split");
 constexpr int kMaxGrid = 148;
 constexpr int kMinRange = 2;                 // key tiles: a shorter range is mostly fill and drain
@@ -71,8 +76,9 @@ struct PreArgs {
     Tile *tiles;
     int cap_tiles;
     Job *jobs;          // [grid]
-    float *rec;         // [grid][2][d + 2][256]
+    float *rec;         // [grid][2][d + 3][256]: O, m, l, m'
     int tpt;            // tokens per 128-row tile
+    int box;            // rows of one copy: 16 to 128 keys of one page
 };
 
 struct Seg {
@@ -180,7 +186,23 @@ paged_plan_kernel(PreArgs a) {
 // Attention
 // ---------------------------------------------------------------------------
 
-// Two e4m3 or int8 codes (bytes i, i + 1 of x) as a bf16 pair, exactly.
+// Four codes as fp16 pairs (bytes 0, 1 and 2, 3), exactly.
+template <int kCode>
+__device__ __forceinline__ void to_h4(uint32_t x, uint32_t &a, uint32_t &b) {
+    if (kCode == SA_E4M3) {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(a), "=r"(b) : "r"(x));
+    } else {
+        // 1024 + (code + 128) under fp16's exponent of 2^10, then minus 1152
+        x ^= 0x80808080u;
+        uint32_t p = __byte_perm(x, 0x64646464u, 0x4140), q = __byte_perm(x, 0x64646464u, 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));
+        const __half2 ha = __hsub2(*reinterpret_cast<__half2 *>(&p), off), hb = __hsub2(*reinterpret_cast<__half2 *>(&q), off);
+        a = *reinterpret_cast<const uint32_t *>(&ha);
+        b = *reinterpret_cast<const uint32_t *>(&hb);
+    }
+}
+// Two codes (bytes 0, 1 or 2, 3 of x) as a bf16 pair, exactly.
 template <int kCode>
 __device__ __forceinline__ uint32_t to_bf2(uint32_t x, bool high) {
     if (kCode == SA_E4M3) {
@@ -209,9 +231,13 @@ enum {
     C_P = C_S + 2,               // [2 Q tiles][4 quarters] P written, 128 arrivals
     C_OD = C_P + 8,              // [2 Q tiles] last PV of the segment done
     C_L = C_OD + 2,              // [2] segment described
-    C_LF = C_L + 2,              // [2] segment released, 13 arrivals
+    C_LF = C_L + 2,              // [2] segment released, 14 arrivals
     C_SC = C_LF + 2,             // [4] scales of a key tile written
-    C_END = C_SC + kScaleSlots,
+    C_RK = C_SC + kScaleSlots,   // codes of K landed
+    C_RV = C_RK + 1,
+    C_RKF = C_RV + 1,            // codes of K read, 4 arrivals
+    C_RVF = C_RKF + 1,
+    C_END = C_RVF + 1,
     NBAR
 };
 
@@ -222,13 +248,17 @@ constexpr uint32_t k_off() { return 2 * tile_bytes<kD>(); }
 template <int kD>
 constexpr uint32_t v_off() { return k_off<kD>() + kStages * tile_bytes<kD>(); }
 template <int kD>
-constexpr uint32_t bar_off() { return v_off<kD>() + kStages * tile_bytes<kD>(); }
+constexpr uint32_t raw_off() { return v_off<kD>() + kStages * tile_bytes<kD>(); }   // codes of K, then of V
 template <int kD>
-constexpr uint32_t smem_bytes() { return bar_off<kD>() + 1024 + 1024; }
+constexpr uint32_t bar_off() { return raw_off<kD>() + 2 * 128 * kD; }
+template <int kD>
+constexpr uint32_t smem_bytes() { return bar_off<kD>() + 2048 + 1024; }
+static_assert(smem_bytes<128>() <= 227 * 1024, "shared memory");
 
 template <int kD, int kCode>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
+paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, PreArgs a) {
     constexpr uint32_t kTile = tile_bytes<kD>();
     const PagedShape &s = a.s;
     extern __shared__ unsigned char pre_raw[];
@@ -239,16 +269,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + bar_off<kD>() + 8 * NBAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_off<kD>() + 8 * NBAR + 4);
     Seg *segs = reinterpret_cast<Seg *>(smem + bar_off<kD>() + 512);                       // [2]
-    float2 *scales = reinterpret_cast<float2 *>(smem + bar_off<kD>() + 640);               // [4][8]: key, value
-    static_assert(8 * NBAR + 8 <= 512 && 2 * sizeof(Seg) <= 128 && 640 + kScaleSlots * 64 <= 1024, "shared memory");
+    // [4][8]: per 16 keys the key scale, the value scale and its log2
+    float4 *scales = reinterpret_cast<float4 *>(smem + bar_off<kD>() + 640);
+    static_assert(8 * NBAR + 8 <= 512 && 2 * sizeof(Seg) <= 128 && 640 + kScaleSlots * 128 <= 2048, "shared memory");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i)
             mbar_init(bar(i), (i >= C_P && i < C_P + 8) ? 128
-                              : (i == C_LF || i == C_LF + 1) ? 13
-                              : (i >= C_KF && i < C_KE) ? 4 : 1);
+                              : (i == C_LF || i == C_LF + 1) ? 14
+                              : (i >= C_KF && i < C_KE) || i == C_RKF || i == C_RVF ? 4 : 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -352,7 +383,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
     } else if (warp == 1) {
         // ---- MMA issuer ------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        constexpr uint32_t idq = idesc_bf16(false, 128), idp = idesc_bf16(true, kD);
+        constexpr uint32_t idq = idesc_bf16(false, 128);
+        constexpr uint32_t idp = idesc_bf16(true, kD) & ~((1u << 7) | (1u << 10));   // fp16 x fp16
         auto qk = [&](int q, int gg) {
             const uint64_t da = desc_k_sw128(sbase + q * kTile);
             const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile);
@@ -363,7 +395,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
             }
             mma_commit_w(bar(C_S + q));
         };
-        // O_q += P_q V for keys 32 h .. 32 h + 31; P_q (bf16) is the first 64 columns of S_q
+        // O_q += P_q V for keys 32 h .. 32 h + 31; P_q (fp16) is the first 64 columns of S_q
         auto pv = [&](int q, int gg, int h, bool acc) {
             const uint64_t db = desc_mn_sw128(sbase + v_off<kD>() + (gg % kStages) * kTile, kChunk);
 #pragma unroll
@@ -436,107 +468,165 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
         mbar_wait(bar(C_END), 0, &never, a.status);
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    } else if (warp < 8) {
-        // ---- converters: cached codes -> bf16 tiles -----------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        constexpr int LPR = kD / 16;              // lanes per row
-        constexpr int RPW = 32 / LPR;             // rows per warp and step
-        constexpr int NS = 128 / (4 * RPW);       // steps per tile
-        const int cw = warp - 4, sub = lane / LPR, l = lane % LPR;
-        const float qs = s.scale * kLog2e;
-        bool ok = true;
-        int gt = 0;
-        for (int n = 0; ok; ++n) {
-            const int slot = n & 1;
-            ok = mbar_wait(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
-            if (!__all_sync(~0u, ok)) break;
-            const Seg g = segs[slot];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C_LF + slot));
-            if (g.tb == g.ta) break;
-            // lane i < 8: page of keys 128 t + 16 i .. + 15 (-1: none)
-            auto page_at = [&](int t) {
-                const int key = 128 * t + 16 * lane;
-                if (lane >= 8 || t >= g.tb || key >= g.n) return -1;
-                const int pg = a.c.table[(size_t)g.b * s.maxb + key / s.bs];
-                if (pg >= 0 && pg < s.pages) return pg;
-                set_status(a.status, kStatusBadIndex);
-                return -1;
-            };
-            // byte offset of the lane's 16 codes in step i of tile t; false: no such key
-            auto where = [&](int t, int pages, int i, size_t &at) {
-                const int r = i * 4 * RPW + cw * RPW + sub, grp = (i * 4 * RPW + cw * RPW) >> 4;
-                const int pg = __shfl_sync(~0u, pages, grp), key = 128 * t + r;
-                at = (((size_t)max(pg, 0) * s.Hkv + g.h) * s.bs + key % s.bs) * kD + l * 16;
-                return pg >= 0 && key < g.n;
-            };
-            auto load = [&](const uint8_t *base, int t, int pages, uint4 *raw) {
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    size_t at;
-                    const bool in = where(t, pages, i, at);
-                    raw[i] = in ? __ldg(reinterpret_cast<const uint4 *>(base + at)) : make_uint4(0, 0, 0, 0);
-                }
-            };
-            auto put = [&](uint32_t tile, const uint4 *raw) {
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const int r = i * 4 * RPW + cw * RPW + sub;
-                    uint4 lo, hi;
-                    lo.x = to_bf2<kCode>(raw[i].x, false);
-                    lo.y = to_bf2<kCode>(raw[i].x, true);
-                    lo.z = to_bf2<kCode>(raw[i].y, false);
-                    lo.w = to_bf2<kCode>(raw[i].y, true);
-                    hi.x = to_bf2<kCode>(raw[i].z, false);
-                    hi.y = to_bf2<kCode>(raw[i].z, true);
-                    hi.z = to_bf2<kCode>(raw[i].w, false);
-                    hi.w = to_bf2<kCode>(raw[i].w, true);
-                    // lanes 4-7 of a 128-wide row fill the other chunk: they
-                    // store their halves in the other order, which keeps the
-                    // eight lanes of a row on different banks
-                    const int u = 2 * (l & 3), swap = l >> 2;
-                    const uint32_t row = tile + swap * kChunk + r * 128;
-                    const uint32_t p0 = row + (((u + swap) ^ (r & 7)) << 4), p1 = row + (((u + 1 - swap) ^ (r & 7)) << 4);
-                    const uint4 v0 = swap ? hi : lo, v1 = swap ? lo : hi;
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p0), "r"(v0.x), "r"(v0.y), "r"(v0.z),
-                                 "r"(v0.w) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p1), "r"(v1.x), "r"(v1.y), "r"(v1.z),
-                                 "r"(v1.w) : "memory");
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (warp == 2) {
+            // ---- codes and scales of each key tile ----------------------------
+            const float qs = s.scale * kLog2e;
+            const int boxes = 128 / a.box;
+            bool ok = true;
+            int gt = 0, klast = -1, vlast = -1;
+            for (int n = 0; ok; ++n) {
+                const int slot = n & 1;
+                ok = mbar_wait(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
+                if (!__all_sync(~0u, ok)) break;
+                const Seg g = segs[slot];
                 __syncwarp();
-            };
-            uint4 kr[NS], vr[NS];
-            int pg = page_at(g.ta), pg1 = page_at(g.ta + 1);
-            load(a.c.K, g.ta, pg, kr);
-            load(a.c.V, g.ta, pg, vr);
-            for (int t = g.ta; t < g.tb; ++t, ++gt) {
-                const int st = gt % kStages, use = gt / kStages;
-                if (gt >= kStages) ok = mbar_wait(bar(C_KE + st), (use - 1) & 1, abort_flag, a.status);
-                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                if (cw == 0) {
-                    if (lane < 8) {
-                        float2 f = make_float2(0.f, 0.f);
-                        if (pg >= 0) {
-                            const size_t ph = (size_t)pg * s.Hkv + g.h;
-                            f = make_float2(a.c.ks[ph], a.c.vs[ph]);
-                        }
+                if (lane == 0) mbar_arrive(bar(C_LF + slot));
+                if (g.tb == g.ta) break;
+                // lane i < 8: page of keys 128 t + 16 i .. + 15 (-1: none), its scales
+                auto page_at = [&](int t) {
+                    const int key = 128 * t + 16 * lane;
+                    return lane < 8 && t < g.tb && key < g.n ? a.c.table[(size_t)g.b * s.maxb + key / s.bs] : -1;
+                };
+                auto scale_at = [&](int &pg, float2 &f) {
+                    f = make_float2(0.f, 0.f);
+                    if (pg < 0 || pg >= s.pages) {
+                        if (pg != -1) set_status(a.status, kStatusBadIndex);
+                        pg = -1;
+                        return;
+                    }
+                    const size_t ph = (size_t)pg * s.Hkv + g.h;
+                    f = make_float2(a.c.ks[ph], a.c.vs[ph]);
+                };
+                int pg = page_at(g.ta), pg1 = page_at(g.ta + 1);
+                float2 f, f1;
+                scale_at(pg, f);
+                for (int t = g.ta; t < g.tb; ++t, ++gt) {
+                    const int pg2 = page_at(t + 2);
+                    scale_at(pg1, f1);
+                    const int key = 128 * t + a.box * lane;
+                    const int mine = __shfl_sync(~0u, pg, (lane * a.box >> 4) & 7);
+                    const bool live = lane < boxes && mine >= 0 && key < g.n;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(~0u, live)) * a.box * kD;
+                    const int y = (mine * s.Hkv + g.h) * s.bs + key % s.bs;
+                    const uint32_t dst = sbase + raw_off<kD>() + lane * a.box * kD;
+                    if (gt >= 1) ok = mbar_wait(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
+                    if (lane < 8)
                         // a key scale of 0 as the smallest number: the mask's -inf survives it
-                        scales[(gt % kScaleSlots) * 8 + lane] = make_float2(fmaxf(f.x * qs, 1.17549435e-38f), f.y);
+                        scales[(gt % kScaleSlots) * 8 + lane] =
+                            make_float4(fmaxf(f.x * qs, 1.17549435e-38f), f.y, log2f(f.y), 0.f);
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(C_SC + gt % kScaleSlots));
+                        if (bytes) mbar_expect_tx(bar(C_RK), bytes);
+                        else mbar_arrive(bar(C_RK));
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C_SC + gt % kScaleSlots));
+                    if (live) tma_load_2d(dst, &tmK, bar(C_RK), 0, y);
+                    klast = gt;
+                    if (gt >= 1) ok = mbar_wait(bar(C_RVF), (gt - 1) & 1, abort_flag, a.status);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
+                    if (lane == 0) {
+                        if (bytes) mbar_expect_tx(bar(C_RV), bytes);
+                        else mbar_arrive(bar(C_RV));
+                    }
+                    __syncwarp();
+                    if (live) tma_load_2d(dst + 128 * kD, &tmV, bar(C_RV), 0, y);
+                    vlast = gt;
+                    pg = pg1;
+                    f = f1;
+                    pg1 = pg2;
                 }
-                put(sbase + k_off<kD>() + st * kTile, kr);
+            }
+            if (lane == 0 && *abort_flag) {
+                // let the copies in flight land before the CTA exits (bounded)
+                volatile int never = 0;
+                if (klast >= 0) mbar_wait(bar(C_RK), klast & 1, &never, a.status);
+                if (vlast >= 0) mbar_wait(bar(C_RV), vlast & 1, &never, a.status);
+            }
+        }
+    } else if (warp < 8) {
+        // ---- converters: codes -> bf16 keys, fp16 values ---------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        constexpr int LPR = kD / 16;              // lanes per row
+        constexpr int NS = 32 / (32 / LPR);       // steps per warp: 32 rows each
+        const int cw = warp - 4, r0 = 32 * cw + lane / LPR, l = lane % LPR;
+        const uint32_t raw = sbase + raw_off<kD>() + 32 * cw * kD + lane * 16;
+        // lanes 4-7 of a 128-wide row fill the other chunk: they store their
+        // halves in the other order, which keeps the eight lanes of a row on
+        // different banks
+        const int u = 2 * (l & 3), swap = l >> 2;
+        bool ok = true;
+        int gt = 0;
+        auto convert = [&](uint32_t src, uint32_t tile, bool key, bool tail, int freed) {
+            uint4 x[NS];
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w) : "r"(src + i * 512));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(freed));
+            if (kCode == SA_E4M3 && !key && tail) {
+                // behind the sequence's end lies any byte, and a NaN must not
+                // meet its weight of 0: those patterns become 256
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    x[i].x -= ((((x[i].x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 7;
+                    x[i].y -= ((((x[i].y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 7;
+                    x[i].z -= ((((x[i].z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 7;
+                    x[i].w -= ((((x[i].w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 7;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int r = r0 + i * (32 / LPR);
+                uint4 lo, hi;
+                if (key) {
+                    lo.x = to_bf2<kCode>(x[i].x, false);
+                    lo.y = to_bf2<kCode>(x[i].x, true);
+                    lo.z = to_bf2<kCode>(x[i].y, false);
+                    lo.w = to_bf2<kCode>(x[i].y, true);
+                    hi.x = to_bf2<kCode>(x[i].z, false);
+                    hi.y = to_bf2<kCode>(x[i].z, true);
+                    hi.z = to_bf2<kCode>(x[i].w, false);
+                    hi.w = to_bf2<kCode>(x[i].w, true);
+                } else {
+                    to_h4<kCode>(x[i].x, lo.x, lo.y);
+                    to_h4<kCode>(x[i].y, lo.z, lo.w);
+                    to_h4<kCode>(x[i].z, hi.x, hi.y);
+                    to_h4<kCode>(x[i].w, hi.z, hi.w);
+                }
+                const uint32_t row = tile + swap * kChunk + r * 128;
+                const uint32_t p0 = row + (((u + swap) ^ (r & 7)) << 4), p1 = row + (((u + 1 - swap) ^ (r & 7)) << 4);
+                const uint4 v0 = swap ? hi : lo, v1 = swap ? lo : hi;
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p0), "r"(v0.x), "r"(v0.y), "r"(v0.z),
+                             "r"(v0.w) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p1), "r"(v1.x), "r"(v1.y), "r"(v1.z),
+                             "r"(v1.w) : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        auto wait = [&](int i, int parity) {
+            return __all_sync(~0u, mbar_wait(bar(i), parity, abort_flag, a.status));
+        };
+        for (int n = 0; ok; ++n) {
+            const int slot = n & 1;
+            if (!(ok = wait(C_L + slot, (n >> 1) & 1))) break;
+            const int ta = segs[slot].ta, tb = segs[slot].tb, keys = segs[slot].n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C_LF + slot));
+            if (ta == tb) break;
+            for (int t = ta; t < tb; ++t, ++gt) {
+                const int st = gt % kStages, use = gt / kStages;
+                if (gt >= kStages && !(ok = wait(C_KE + st, (use - 1) & 1))) break;
+                if (!(ok = wait(C_RK, gt & 1))) break;
+                convert(raw, sbase + k_off<kD>() + st * kTile, true, false, C_RKF);
                 if (lane == 0) mbar_arrive(bar(C_KF + st));
-                if (t + 1 < g.tb) load(a.c.K, t + 1, pg1, kr);
-                if (gt >= kStages) ok = mbar_wait(bar(C_VE + st), (use - 1) & 1, abort_flag, a.status);
-                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                put(sbase + v_off<kD>() + st * kTile, vr);
+                if (gt >= kStages && !(ok = wait(C_VE + st, (use - 1) & 1))) break;
+                if (!(ok = wait(C_RV, gt & 1))) break;
+                convert(raw + 128 * kD, sbase + v_off<kD>() + st * kTile, false, 128 * (t + 1) > keys, C_RVF);
                 if (lane == 0) mbar_arrive(bar(C_VF + st));
-                if (t + 1 < g.tb) load(a.c.V, t + 1, pg1, vr);
-                pg = pg1;
-                pg1 = page_at(t + 2);
             }
         }
     } else {
@@ -564,7 +654,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
             const int tok = q * a.tpt + tok_r;
             const bool row_ok = tok_r < a.tpt && tok < g.ntok;
             const int see = s.flags & SA_CAUSAL ? max(0, min(g.n, g.pos0 + tok + 1)) : g.n;
-            float m_run = -CUDART_INF_F, l = 0.f;
+            float m_run = -CUDART_INF_F, mv_run = -CUDART_INF_F, l = 0.f;   // references of l and of O
             for (int t = g.ta; t < g.tb; ++t, ++gt, ++gp) {
                 ok = mbar_wait(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status) &&
                      mbar_wait(bar(C_S + q), gp & 1, abort_flag, a.status);
@@ -575,14 +665,14 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
                 for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
                 tmem_wait_ld();
                 reg_fence<128>(x);
-                const float2 *sc = scales + (gt % kScaleSlots) * 8;
+                const float4 *sc = scales + (gt % kScaleSlots) * 8;
                 const int vis = see - 128 * t;             // keys of this tile the row sees
                 if (vis < 128) {
 #pragma unroll
                     for (int k = 0; k < 128; ++k) x[k] = k < vis ? x[k] : -CUDART_INF_F;
                 }
                 // 16 keys share a page, so a scale: the largest logit of each group
-                float mx = -CUDART_INF_F;
+                float mx = -CUDART_INF_F, mv = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float m0 = fmax3(x[16 * i], x[16 * i + 1], x[16 * i + 2]);
@@ -592,18 +682,25 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
                     m0 = fmax3(m0, x[16 * i + 10], x[16 * i + 11]);
                     m1 = fmax3(m1, x[16 * i + 12], x[16 * i + 13]);
                     m0 = fmax3(m0, x[16 * i + 14], x[16 * i + 15]);
-                    mx = fmaxf(mx, fmaxf(m0, m1) * sc[i].x);
+                    const float4 f = sc[i];
+                    const float z = fmaxf(m0, m1) * f.x;
+                    mx = fmaxf(mx, z);
+                    mv = fmaxf(mv, z + f.z);
                 }
                 if (t == g.ta) {
                     m_run = mx;
+                    mv_run = mv;
                 } else {
-                    const bool need = mx > m_run + 8.f;
+                    const bool need = mx > m_run + 8.f || mv > mv_run + 8.f;
                     if (__any_sync(~0u, need)) {
                         // the PV before this S has completed: O is stable
-                        const float corr = need ? ex2(m_run - mx) : 1.f;
+                        float corr = 1.f;
                         if (need) {
-                            l *= corr;
-                            m_run = mx;
+                            const float m1 = fmaxf(mx, m_run), v1 = fmaxf(mv, mv_run);
+                            l *= m_run == m1 ? 1.f : ex2(m_run - m1);
+                            corr = mv_run == v1 ? 1.f : ex2(mv_run - v1);
+                            m_run = m1;
+                            mv_run = v1;
                         }
 #pragma unroll
                         for (int cc = 0; cc < kD / 32; ++cc) {
@@ -620,14 +717,18 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
                 }
                 const float ref = m_run == -CUDART_INF_F ? 0.f : m_run;
                 const float2 b2 = make_float2(-ref, -ref);
+                // p vs 2^(m - m'); the limit keeps the factor of keys whose p
+                // is 0 finite
+                const float vf = mv_run == -CUDART_INF_F ? 0.f : ref - mv_run;
                 float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 f = sc[2 * c + i];
-                        const float2 sk = make_float2(f.x, f.x), sv = make_float2(f.y, f.y);
+                        const float4 f = sc[2 * c + i];
+                        const float v = ex2(fminf(f.z + vf, 126.f));
+                        const float2 sk = make_float2(f.x, f.x), sv = make_float2(v, v);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int e = 32 * c + 16 * i + 2 * k;
@@ -635,8 +736,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
                             float2 p = make_float2(ex2(z.x), ex2(z.y));
                             if (k & 1) lb = fadd2(lb, p);
                             else la = fadd2(la, p);
-                            p = ffma2(p, sv, make_float2(0.f, 0.f));
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+                            p = fmul2(p, sv);
+                            const __half2 h2 = __floats2half2_rn(p.x, p.y);
                             pk[8 * i + k] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
                     }
@@ -654,8 +755,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
             ++done;
             tc_fence_after();
             const size_t row = row_ok ? (size_t)(g.row0 + tok) * s.Hq + g.h * s.G + head_r : 0;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            float *rec = a.rec + ((size_t)blockIdx.x * 2 + (g.out == 2 ? 1 : 0)) * (kD + 2) * 256 + 128 * q + r;
+            const float inv = l == 0.f || mv_run == -CUDART_INF_F ? 0.f : ex2(mv_run - m_run) / l;
+            float *rec = a.rec + ((size_t)blockIdx.x * 2 + (g.out == 2 ? 1 : 0)) * (kD + 3) * 256 + 128 * q + r;
 #pragma unroll
             for (int cc = 0; cc < kD / 32; ++cc) {
                 float o[32];
@@ -682,6 +783,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PreArgs a) {
                 } else {
                     rec[(size_t)kD * 256] = m_run;
                     rec[(size_t)(kD + 1) * 256] = l;
+                    rec[(size_t)(kD + 2) * 256] = mv_run;
                 }
             }
         }
@@ -707,20 +809,23 @@ paged_prefill_merge_kernel(PreArgs a) {
     const int warp = threadIdx.x >> 5, r = 32 * blockIdx.y + (threadIdx.x & 31);
     const int q = r >> 7, tok_r = (r & 127) / a.s.G, head = (r & 127) - tok_r * a.s.G, tok = q * a.tpt + tok_r;
     if (tok_r >= a.tpt || tok >= job.ntok) return;
-    auto rec = [&](int i) { return a.rec + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * (kD + 2) * 256 + r; };
-    float M = -CUDART_INF_F, l = 0.f, o[NC];
-    for (int i = 0; i < job.n; ++i) M = fmaxf(M, rec(i)[kD * 256]);
+    auto rec = [&](int i) { return a.rec + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * (kD + 3) * 256 + r; };
+    float M = -CUDART_INF_F, MV = -CUDART_INF_F, l = 0.f, o[NC];
+    for (int i = 0; i < job.n; ++i) {
+        M = fmaxf(M, rec(i)[kD * 256]);
+        MV = fmaxf(MV, rec(i)[(kD + 2) * 256]);
+    }
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = 0.f;
     for (int i = 0; i < job.n; ++i) {
         const float *p = rec(i);
-        const float m = p[kD * 256], f = m == -CUDART_INF_F ? 0.f : ex2(m - M);
-        l += p[(kD + 1) * 256] * f;
+        const float m = p[kD * 256], v = p[(kD + 2) * 256], f = v == -CUDART_INF_F ? 0.f : ex2(v - MV);
+        l += m == -CUDART_INF_F ? 0.f : p[(kD + 1) * 256] * ex2(m - M);
 #pragma unroll
         for (int k = 0; k < NC; ++k) o[k] += p[(warp * NC + k) * 256] * f;
     }
     const size_t row = (size_t)(job.row0 + tok) * a.s.Hq + job.h * a.s.G + head;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f || MV == -CUDART_INF_F ? 0.f : ex2(MV - M) / l;
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = l == 0.f ? 0.f : o[k] * inv;
 #pragma unroll
@@ -732,7 +837,8 @@ size_t al(size_t x) { return (x + 255) & ~(size_t)255; }
 int cap_tiles(const PagedShape &s) { return s.tokens / (2 * (128 / s.G)) + s.B + 1; }
 
 template <int kD, int kCode>
-cudaError_t run(const PreArgs &a, int grid, const CUtensorMap &mq, cudaStream_t st) {
+cudaError_t run(const PreArgs &a, int grid, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                cudaStream_t st) {
     auto kern = paged_prefill_kernel<kD, kCode>;
     // the register split assumes the launch's count
     cudaFuncAttributes fa;
@@ -748,7 +854,7 @@ cudaError_t run(const PreArgs &a, int grid, const CUtensorMap &mq, cudaStream_t 
     }
     if ((e = launch_pdl(paged_plan_kernel, dim3(1), dim3(1024), plan_smem, st, a)) != cudaSuccess) return e;
     note_launch();
-    if ((e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem_bytes<kD>(), st, mq, a)) != cudaSuccess)
+    if ((e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem_bytes<kD>(), st, mq, mk, mv, a)) != cudaSuccess)
         return e;
     note_launch();
     if ((e = launch_pdl(paged_prefill_merge_kernel<kD>, dim3((unsigned)grid, 8), dim3(256), 0, st, a)) != cudaSuccess)
@@ -763,7 +869,7 @@ bool paged_prefill_supported(const PagedShape &s) { return s.dtype == SA_BF16 &&
 
 size_t paged_prefill_scratch(const PagedShape &s) {
     return al(sizeof(PlanHead)) + al(cap_tiles(s) * sizeof(Tile)) + al(kMaxGrid * sizeof(Job)) +
-           (size_t)kMaxGrid * 2 * (s.d + 2) * 256 * sizeof(float);
+           (size_t)kMaxGrid * 2 * (s.d + 3) * 256 * sizeof(float);
 }
 
 cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32_t *cu, const PagedCache &c, void *O,
@@ -798,10 +904,22 @@ cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
+    // codes as they lie; a box is the largest power of two of keys in one page
+    a.box = s.bs & -s.bs;
+    CUtensorMap mk, mv;
+    cuuint64_t cdims[2] = {(cuuint64_t)s.d, (cuuint64_t)s.pages * s.Hkv * s.bs};
+    cuuint64_t cstrides[1] = {(cuuint64_t)s.d};
+    cuuint32_t cbox[2] = {(cuuint32_t)s.d, (cuuint32_t)a.box};
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(i ? c.V : c.K), cdims, cstrides,
+                cbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
     const int grid = min(sms, kMaxGrid);
     if (s.d == 128)
-        return s.code == SA_E4M3 ? run<128, SA_E4M3>(a, grid, mq, st) : run<128, SA_INT8>(a, grid, mq, st);
-    return s.code == SA_E4M3 ? run<64, SA_E4M3>(a, grid, mq, st) : run<64, SA_INT8>(a, grid, mq, st);
+        return s.code == SA_E4M3 ? run<128, SA_E4M3>(a, grid, mq, mk, mv, st)
+                                 : run<128, SA_INT8>(a, grid, mq, mk, mv, st);
+    return s.code == SA_E4M3 ? run<64, SA_E4M3>(a, grid, mq, mk, mv, st) : run<64, SA_INT8>(a, grid, mq, mk, mv, st);
 }
 
 }  // namespace sa
