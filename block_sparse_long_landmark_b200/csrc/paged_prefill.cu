@@ -10,10 +10,13 @@
 // core runs the other's products.  Tensor work 4 rows d flops a key against
 // d conversions a key and d bytes: tensor and exponential bound at 256 rows,
 // cache-read bound when a chunk has few.
-//   * TMA brings a tile's codes from its pages to shared memory; a converter
-//     warpgroup makes bf16 keys (as the queries are) and fp16 values of them,
-//     both exactly.  Scales stay out of the matrices: the key's multiplies the
-//     logit, the value's the weight;
+//   * TMA brings a tile's codes from its pages to shared memory, and a
+//     converter warpgroup makes fp16 of them, exactly and with one conversion
+//     instruction per two codes (bf16 takes five).  The launch before has put
+//     the queries into fp16, each row scaled by a power of two so that its
+//     largest element lies in [2^14, 2^15): what falls below fp16's range is
+//     under 2^-38 of it.  Scales stay out of the matrices: the key's and the
+//     row's multiply the logit, the value's the weight;
 //   * weights are rounded to fp16 (2^-11 of each).  p vs spans the scales'
 //     range, so O has a reference of its own: with m the row's largest logit
 //     and m' its largest logit + log2 vs, l sums p = 2^(z - m) and the tensor
@@ -76,6 +79,9 @@ struct PreArgs {
     Tile *tiles;
     int cap_tiles;
     Job *jobs;          // [grid]
+    const __nv_bfloat16 *Q;
+    __half *qh;         // [tokens][Hq][d] queries in fp16
+    float *qf;          // [tokens][Hq] logit scale of a row of qh, log2 units
     float *rec;         // [grid][2][d + 3][256]: O, m, l, m'
     int tpt;            // tokens per 128-row tile
     int box;            // rows of one copy: 16 to 128 keys of one page
@@ -90,8 +96,8 @@ struct Seg {
 };
 
 // ---------------------------------------------------------------------------
-// The step list: units in order of (sequence, token), each with its number of
-// key tiles and the tiles before it.  One CTA.
+// CTA 0: the step list: units in order of (sequence, token), each with its
+// number of key tiles and the tiles before it.  The others: fp16 queries.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int last_le(const int *off, int n, int x) {
     int lo = 0, hi = n;
@@ -136,6 +142,34 @@ paged_plan_kernel(PreArgs a) {
     const int tid = threadIdx.x, tpu = 2 * a.tpt;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x > 0) {
+        // a row per half warp or quarter: d / 8 lanes of eight elements
+        const int lpr = s.d / 8, l = tid % lpr;
+        const long long rows = (long long)max(0, min(a.cu[s.B], s.tokens)) * s.Hq;
+        const long long step = (long long)(gridDim.x - 1) * (1024 / lpr);
+        long long row = (long long)(blockIdx.x - 1) * (1024 / lpr) + tid / lpr;
+        for (const long long end = (rows + 3) / 4 * 4; row < end; row += step) {   // whole warps
+            const bool in = row < rows;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (in) x = *reinterpret_cast<const uint4 *>(a.Q + row * s.d + 8 * l);
+            unsigned big = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                    __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+            big = max(big & 0xffffu, big >> 16);
+            for (int o = 1; o < lpr; o <<= 1) big = max(big, __shfl_xor_sync(~0u, big, o));
+            const int up = max(-113, min(126, 14 - ((int)(big >> 7) - 127)));
+            const float f = __uint_as_float((unsigned)(up + 127) << 23);
+            float v[8];
+            load16(reinterpret_cast<const __nv_bfloat16 *>(&x), v);
+            __half2 h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
+            if (in) {
+                *reinterpret_cast<uint4 *>(a.qh + row * s.d + 8 * l) = *reinterpret_cast<const uint4 *>(h);
+                if (l == 0) a.qf[row] = s.scale * kLog2e * __uint_as_float((unsigned)(127 - up) << 23);
+            }
+        }
+        return;
+    }
     const int share = (s.B + 1023) / 1024, b0 = min(s.B, tid * share), b1 = min(s.B, b0 + share);
     long long n = 0, total;
     for (int b = b0; b < b1; ++b) {
@@ -202,23 +236,8 @@ __device__ __forceinline__ void to_h4(uint32_t x, uint32_t &a, uint32_t &b) {
         b = *reinterpret_cast<const uint32_t *>(&hb);
     }
 }
-// Two codes (bytes 0, 1 or 2, 3 of x) as a bf16 pair, exactly.
-template <int kCode>
-__device__ __forceinline__ uint32_t to_bf2(uint32_t x, bool high) {
-    if (kCode == SA_E4M3) {
-        // sign and seven value bits under bf16's 8-bit exponent give value * 2^-120
-        const uint32_t w = __byte_perm(x, 0, high ? 0x3424 : 0x1404);
-        uint32_t v = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-        const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7b80));   // 2^120
-        __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&v), up);
-        return *reinterpret_cast<uint32_t *>(&r);
-    }
-    // 128 + low seven bits, minus 128 or (sign bit: the exponent's lowest) 256
-    const uint32_t w = __byte_perm(x, 0x43434343u, high ? 0x4342 : 0x4140);
-    uint32_t lo = w & 0xff7fff7fu, off = w & 0xff80ff80u;
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&lo), *reinterpret_cast<__nv_bfloat162 *>(&off));
-    return *reinterpret_cast<uint32_t *>(&r);
-}
+// Key scale times row scale, never 0: the mask's -inf survives it.
+__device__ __forceinline__ float logit_scale(float ks, float qf) { return fmaxf(ks * qf, 1.17549435e-38f); }
 
 enum {
     C_Q = 0,                     // Q tiles landed (one phase per segment)
@@ -228,7 +247,7 @@ enum {
     C_KE = C_VF + kStages,       // [2] K stage free
     C_VE = C_KE + kStages,
     C_S = C_VE + kStages,        // [2 Q tiles] S ready
-    C_P = C_S + 2,               // [2 Q tiles][4 quarters] P written, 128 arrivals
+    C_P = C_S + 2,               // [2 Q tiles][4 quarters] P written, 4 arrivals
     C_OD = C_P + 8,              // [2 Q tiles] last PV of the segment done
     C_L = C_OD + 2,              // [2] segment described
     C_LF = C_L + 2,              // [2] segment released, 14 arrivals
@@ -277,7 +296,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i)
-            mbar_init(bar(i), (i >= C_P && i < C_P + 8) ? 128
+            mbar_init(bar(i), (i >= C_P && i < C_P + 8) ? 4
                               : (i == C_LF || i == C_LF + 1) ? 14
                               : (i >= C_KF && i < C_KE) || i == C_RKF || i == C_RVF ? 4 : 1);
         *abort_flag = 0;
@@ -383,8 +402,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     } else if (warp == 1) {
         // ---- MMA issuer ------------------------------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        constexpr uint32_t idq = idesc_bf16(false, 128);
-        constexpr uint32_t idp = idesc_bf16(true, kD) & ~((1u << 7) | (1u << 10));   // fp16 x fp16
+        constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));     // the operand formats' bits: fp16 instead of bf16
+        constexpr uint32_t idq = idesc_bf16(false, 128) & kFp16, idp = idesc_bf16(true, kD) & kFp16;
         auto qk = [&](int q, int gg) {
             const uint64_t da = desc_k_sw128(sbase + q * kTile);
             const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile);
@@ -470,7 +489,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == 2) {
             // ---- codes and scales of each key tile ----------------------------
-            const float qs = s.scale * kLog2e;
             const int boxes = 128 / a.box;
             bool ok = true;
             int gt = 0, klast = -1, vlast = -1;
@@ -512,9 +530,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     if (gt >= 1) ok = mbar_wait(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
                     if (!__all_sync(~0u, ok)) { ok = false; break; }
                     if (lane < 8)
-                        // a key scale of 0 as the smallest number: the mask's -inf survives it
-                        scales[(gt % kScaleSlots) * 8 + lane] =
-                            make_float4(fmaxf(f.x * qs, 1.17549435e-38f), f.y, log2f(f.y), 0.f);
+                        scales[(gt % kScaleSlots) * 8 + lane] = make_float4(f.x, f.y, log2f(f.y), 0.f);
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(C_SC + gt % kScaleSlots));
@@ -546,7 +562,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             }
         }
     } else if (warp < 8) {
-        // ---- converters: codes -> bf16 keys, fp16 values ---------------------
+        // ---- converters: codes -> fp16 tiles -----------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
         constexpr int LPR = kD / 16;              // lanes per row
         constexpr int NS = 32 / (32 / LPR);       // steps per warp: 32 rows each
@@ -558,7 +574,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         const int u = 2 * (l & 3), swap = l >> 2;
         bool ok = true;
         int gt = 0;
-        auto convert = [&](uint32_t src, uint32_t tile, bool key, bool tail, int freed) {
+        auto convert = [&](uint32_t src, uint32_t tile, bool tail, int freed) {
             uint4 x[NS];
 #pragma unroll
             for (int i = 0; i < NS; ++i)
@@ -566,7 +582,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                              : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w) : "r"(src + i * 512));
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(freed));
-            if (kCode == SA_E4M3 && !key && tail) {
+            if (kCode == SA_E4M3 && tail) {
                 // behind the sequence's end lies any byte, and a NaN must not
                 // meet its weight of 0: those patterns become 256
 #pragma unroll
@@ -581,21 +597,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             for (int i = 0; i < NS; ++i) {
                 const int r = r0 + i * (32 / LPR);
                 uint4 lo, hi;
-                if (key) {
-                    lo.x = to_bf2<kCode>(x[i].x, false);
-                    lo.y = to_bf2<kCode>(x[i].x, true);
-                    lo.z = to_bf2<kCode>(x[i].y, false);
-                    lo.w = to_bf2<kCode>(x[i].y, true);
-                    hi.x = to_bf2<kCode>(x[i].z, false);
-                    hi.y = to_bf2<kCode>(x[i].z, true);
-                    hi.z = to_bf2<kCode>(x[i].w, false);
-                    hi.w = to_bf2<kCode>(x[i].w, true);
-                } else {
-                    to_h4<kCode>(x[i].x, lo.x, lo.y);
-                    to_h4<kCode>(x[i].y, lo.z, lo.w);
-                    to_h4<kCode>(x[i].z, hi.x, hi.y);
-                    to_h4<kCode>(x[i].w, hi.z, hi.w);
-                }
+                to_h4<kCode>(x[i].x, lo.x, lo.y);
+                to_h4<kCode>(x[i].y, lo.z, lo.w);
+                to_h4<kCode>(x[i].z, hi.x, hi.y);
+                to_h4<kCode>(x[i].w, hi.z, hi.w);
                 const uint32_t row = tile + swap * kChunk + r * 128;
                 const uint32_t p0 = row + (((u + swap) ^ (r & 7)) << 4), p1 = row + (((u + 1 - swap) ^ (r & 7)) << 4);
                 const uint4 v0 = swap ? hi : lo, v1 = swap ? lo : hi;
@@ -621,11 +626,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 const int st = gt % kStages, use = gt / kStages;
                 if (gt >= kStages && !(ok = wait(C_KE + st, (use - 1) & 1))) break;
                 if (!(ok = wait(C_RK, gt & 1))) break;
-                convert(raw, sbase + k_off<kD>() + st * kTile, true, false, C_RKF);
+                convert(raw, sbase + k_off<kD>() + st * kTile, false, C_RKF);
                 if (lane == 0) mbar_arrive(bar(C_KF + st));
                 if (gt >= kStages && !(ok = wait(C_VE + st, (use - 1) & 1))) break;
                 if (!(ok = wait(C_RV, gt & 1))) break;
-                convert(raw + 128 * kD, sbase + v_off<kD>() + st * kTile, false, 128 * (t + 1) > keys, C_RVF);
+                convert(raw + 128 * kD, sbase + v_off<kD>() + st * kTile, 128 * (t + 1) > keys, C_RVF);
                 if (lane == 0) mbar_arrive(bar(C_VF + st));
             }
         }
@@ -642,20 +647,23 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             const int slot = n & 1;
             ok = mbar_wait(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
             if (!__all_sync(~0u, ok)) break;
-            const Seg g = segs[slot];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C_LF + slot));
+            const Seg &g = segs[slot];      // released at the segment's end
             const int T = g.tb - g.ta;
             if (T == 0) break;
             if (q >= g.nq) {
                 gt += T;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C_LF + slot));
                 continue;
             }
             const int tok = q * a.tpt + tok_r;
             const bool row_ok = tok_r < a.tpt && tok < g.ntok;
-            const int see = s.flags & SA_CAUSAL ? max(0, min(g.n, g.pos0 + tok + 1)) : g.n;
+            // keys the row sees, from the segment's first tile on
+            int vis = (s.flags & SA_CAUSAL ? max(0, min(g.n, g.pos0 + tok + 1)) : g.n) - 128 * g.ta;
+            const size_t row = row_ok ? (size_t)(g.row0 + tok) * s.Hq + g.h * s.G + head_r : 0;
+            const float qf = row_ok ? a.qf[row] : 0.f;
             float m_run = -CUDART_INF_F, mv_run = -CUDART_INF_F, l = 0.f;   // references of l and of O
-            for (int t = g.ta; t < g.tb; ++t, ++gt, ++gp) {
+            for (int t = 0; t < T; ++t, ++gt, ++gp, vis -= 128) {
                 ok = mbar_wait(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status) &&
                      mbar_wait(bar(C_S + q), gp & 1, abort_flag, a.status);
                 if (!__all_sync(~0u, ok)) { ok = false; break; }
@@ -666,7 +674,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 tmem_wait_ld();
                 reg_fence<128>(x);
                 const float4 *sc = scales + (gt % kScaleSlots) * 8;
-                const int vis = see - 128 * t;             // keys of this tile the row sees
                 if (vis < 128) {
 #pragma unroll
                     for (int k = 0; k < 128; ++k) x[k] = k < vis ? x[k] : -CUDART_INF_F;
@@ -683,11 +690,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     m1 = fmax3(m1, x[16 * i + 12], x[16 * i + 13]);
                     m0 = fmax3(m0, x[16 * i + 14], x[16 * i + 15]);
                     const float4 f = sc[i];
-                    const float z = fmaxf(m0, m1) * f.x;
+                    const float z = fmaxf(m0, m1) * logit_scale(f.x, qf);
                     mx = fmaxf(mx, z);
                     mv = fmaxf(mv, z + f.z);
                 }
-                if (t == g.ta) {
+                if (t == 0) {
                     m_run = mx;
                     mv_run = mv;
                 } else {
@@ -728,7 +735,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     for (int i = 0; i < 2; ++i) {
                         const float4 f = sc[2 * c + i];
                         const float v = ex2(fminf(f.z + vf, 126.f));
-                        const float2 sk = make_float2(f.x, f.x), sv = make_float2(v, v);
+                        const float k1 = logit_scale(f.x, qf);
+                        const float2 sk = make_float2(k1, k1), sv = make_float2(v, v);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int e = 32 * c + 16 * i + 2 * k;
@@ -744,7 +752,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     tmem_st16(tS + 16 * c, pk);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(bar(C_P + 4 * q + c));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C_P + 4 * q + c));
                 }
                 l += (la.x + la.y) + (lb.x + lb.y);
             }
@@ -754,7 +763,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             ++done;
             tc_fence_after();
-            const size_t row = row_ok ? (size_t)(g.row0 + tok) * s.Hq + g.h * s.G + head_r : 0;
             const float inv = l == 0.f || mv_run == -CUDART_INF_F ? 0.f : ex2(mv_run - m_run) / l;
             float *rec = a.rec + ((size_t)blockIdx.x * 2 + (g.out == 2 ? 1 : 0)) * (kD + 3) * 256 + 128 * q + r;
 #pragma unroll
@@ -786,6 +794,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     rec[(size_t)(kD + 2) * 256] = mv_run;
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C_LF + slot));
         }
     }
 
@@ -852,7 +862,9 @@ cudaError_t run(const PreArgs &a, int grid, const CUtensorMap &mq, const CUtenso
         e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem);
         if (e != cudaSuccess) return e;
     }
-    if ((e = launch_pdl(paged_plan_kernel, dim3(1), dim3(1024), plan_smem, st, a)) != cudaSuccess) return e;
+    // queries: up to one CTA per SM beside the one that lists the steps
+    const long long conv = ((long long)a.s.tokens * a.s.Hq * a.s.d / 8 + 1023) / 1024;
+    if ((e = launch_pdl(paged_plan_kernel, dim3(1 + (unsigned)min(conv, (long long)grid)), dim3(1024), plan_smem, st, a)) != cudaSuccess) return e;
     note_launch();
     if ((e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem_bytes<kD>(), st, mq, mk, mv, a)) != cudaSuccess)
         return e;
@@ -868,7 +880,7 @@ cudaError_t run(const PreArgs &a, int grid, const CUtensorMap &mq, const CUtenso
 bool paged_prefill_supported(const PagedShape &s) { return s.dtype == SA_BF16 && s.G <= 128; }
 
 size_t paged_prefill_scratch(const PagedShape &s) {
-    return al(sizeof(PlanHead)) + al(cap_tiles(s) * sizeof(Tile)) + al(kMaxGrid * sizeof(Job)) +
+    return al((size_t)s.tokens * s.Hq * s.d * 2) + al((size_t)s.tokens * s.Hq * 4) + al(sizeof(PlanHead)) + al(cap_tiles(s) * sizeof(Tile)) + al(kMaxGrid * sizeof(Job)) +
            (size_t)kMaxGrid * 2 * (s.d + 3) * 256 * sizeof(float);
 }
 
@@ -884,6 +896,11 @@ cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32
     a.tpt = 128 / s.G;
     a.cap_tiles = cap_tiles(s);
     unsigned char *w = (unsigned char *)scratch;
+    a.Q = (const __nv_bfloat16 *)Q;
+    a.qh = (__half *)w;
+    w += al((size_t)s.tokens * s.Hq * s.d * 2);
+    a.qf = (float *)w;
+    w += al((size_t)s.tokens * s.Hq * 4);
     a.head = (PlanHead *)w;
     w += al(sizeof(PlanHead));
     a.tiles = (Tile *)w;
@@ -900,7 +917,7 @@ cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32
     cuuint64_t strides[2] = {(cuuint64_t)s.d * 2, (cuuint64_t)s.Hq * s.d * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)s.G, (cuuint32_t)a.tpt};
     cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(Q), dims, strides, box, estr,
+    if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.qh, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
