@@ -28,8 +28,10 @@
 //     share leave fp32 records (at most two a CTA), joined by a second launch.
 //
 // Warps: 0 takes segments from the line and loads Q by TMA, 1 owns tensor
-// memory and issues the MMAs, 2 loads codes and scales, 3 idles; 4-7 convert;
-// 8-11 and 12-15 softmax.
+// memory and issues the MMAs of Q tile 0, 3 those of Q tile 1 (one warp for
+// both would hold one tile's products back while it waits, quarter by quarter,
+// for the other's weights: 3.39 against ... ms for the 4K chunk at 32K), 2
+// loads codes and scales; 4-7 convert; 8-11 and 12-15 softmax.
 // Registers: launched at 128; 56 + 88 + 2 * 184 = 4 * 128.
 // Every wait is bounded; when one runs out the CTA sets the status word, lets
 // its copies land, frees tensor memory and exits.
@@ -241,23 +243,23 @@ __device__ __forceinline__ float logit_scale(float ks, float qf) { return fmaxf(
 
 enum {
     C_Q = 0,                     // Q tiles landed (one phase per segment)
-    C_QFREE = 1,                 // every QK of the segment done
+    C_QFREE = 1,                 // every QK of the segment done, 2 arrivals
     C_KF = 2,                    // [2] K tile converted, 4 arrivals
     C_VF = C_KF + kStages,       // [2]
-    C_KE = C_VF + kStages,       // [2] K stage free
+    C_KE = C_VF + kStages,       // [2] K stage free, 2 arrivals (one per Q tile)
     C_VE = C_KE + kStages,
     C_S = C_VE + kStages,        // [2 Q tiles] S ready
     C_P = C_S + 2,               // [2 Q tiles][4 quarters] P written, 4 arrivals
     C_OD = C_P + 8,              // [2 Q tiles] last PV of the segment done
     C_L = C_OD + 2,              // [2] segment described
-    C_LF = C_L + 2,              // [2] segment released, 14 arrivals
+    C_LF = C_L + 2,              // [2] segment released, 15 arrivals
     C_SC = C_LF + 2,             // [4] scales of a key tile written
     C_RK = C_SC + kScaleSlots,   // codes of K landed
     C_RV = C_RK + 1,
     C_RKF = C_RV + 1,            // codes of K read, 4 arrivals
     C_RVF = C_RKF + 1,
-    C_END = C_RVF + 1,
-    NBAR
+    C_END = C_RVF + 1,           // [2 Q tiles]
+    NBAR = C_END + 2
 };
 
 template <int kD>
@@ -297,7 +299,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i)
             mbar_init(bar(i), (i >= C_P && i < C_P + 8) ? 4
-                              : (i == C_LF || i == C_LF + 1) ? 14
+                              : (i == C_LF || i == C_LF + 1) ? 15
+                              : (i >= C_KE && i < C_S) || i == C_QFREE ? 2
                               : (i >= C_KF && i < C_KE) || i == C_RKF || i == C_RVF ? 4 : 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -355,13 +358,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 g.out = g.tb - g.ta == t.kt ? 0 : g.ta > 0 ? 1 : 2;
                 if (g.out == 2) job = Job{(int)((u0 + t.kt - 1) / per) - (int)blockIdx.x + 1, g.row0, g.ntok, h};
                 const int slot = n & 1;
-                if (n >= 2) ok = mbar_wait(bar(C_LF + slot), ((n >> 1) - 1) & 1, abort_flag, a.status);
+                if (n >= 2) ok = mbar_wait_lazy(bar(C_LF + slot), ((n >> 1) - 1) & 1, abort_flag, a.status);
                 if (!__all_sync(~0u, ok)) { ok = false; break; }
                 if (lane == 0) {
                     segs[slot] = g;
                     mbar_arrive(bar(C_L + slot));
                     // Q: the group's heads of the unit's tokens, token-major rows
-                    if (n >= 1) ok = mbar_wait(bar(C_QFREE), (n - 1) & 1, abort_flag, a.status);
+                    if (n >= 1) ok = mbar_wait_lazy(bar(C_QFREE), (n - 1) & 1, abort_flag, a.status);
                     if (ok) {
                         mbar_expect_tx(bar(C_Q), (uint32_t)(g.nq * (kD / 64) * a.tpt * s.G * 128));
                         for (int q = 0; q < g.nq; ++q)
@@ -389,7 +392,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         if (ok) {
             // the end: a segment without tiles
             const int slot = n & 1;
-            if (n >= 2) ok = mbar_wait(bar(C_LF + slot), ((n >> 1) - 1) & 1, abort_flag, a.status);
+            if (n >= 2) ok = mbar_wait_lazy(bar(C_LF + slot), ((n >> 1) - 1) & 1, abort_flag, a.status);
             if (__all_sync(~0u, ok) && lane == 0) {
                 segs[slot].ta = segs[slot].tb = 0;
                 mbar_arrive(bar(C_L + slot));
@@ -397,104 +400,99 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         }
         if (lane == 0 && *abort_flag && qlast >= 0) {
             volatile int never = 0;
-            mbar_wait(bar(C_Q), qlast & 1, &never, a.status);
+            mbar_wait_lazy(bar(C_Q), qlast & 1, &never, a.status);
         }
-    } else if (warp == 1) {
-        // ---- MMA issuer ------------------------------------------------------
+    } else if (warp == 1 || warp == 3) {
+        // ---- MMA issuers: Q tile 0 and Q tile 1 --------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));     // the operand formats' bits: fp16 instead of bf16
         constexpr uint32_t idq = idesc_bf16(false, 128) & kFp16, idp = idesc_bf16(true, kD) & kFp16;
-        auto qk = [&](int q, int gg) {
-            const uint64_t da = desc_k_sw128(sbase + q * kTile);
+        const int q = warp >> 1;
+        const uint32_t tS = tmem + q * 128, tO = tmem + 256 + q * 128;
+        const uint64_t dq = desc_k_sw128(sbase + q * kTile);
+        auto qk = [&](int gg) {
             const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile);
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
                 const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-                mma_ss_w(tmem + q * 128, da + off, db + off, idq, k > 0);
+                mma_ss_w(tS, dq + off, db + off, idq, k > 0);
             }
             mma_commit_w(bar(C_S + q));
+            mma_commit_w(bar(C_KE + gg % kStages));
         };
-        // O_q += P_q V for keys 32 h .. 32 h + 31; P_q (fp16) is the first 64 columns of S_q
-        auto pv = [&](int q, int gg, int h, bool acc) {
+        // O += P V for keys 32 h .. 32 h + 31; P (fp16) is the first 64 columns of S
+        auto pv = [&](int gg, int h, bool acc) {
             const uint64_t db = desc_mn_sw128(sbase + v_off<kD>() + (gg % kStages) * kTile, kChunk);
 #pragma unroll
             for (int k = 2 * h; k < 2 * h + 2; ++k)
-                mma_ts_w(tmem + 256 + q * 128, tmem + q * 128 + 8 * k, db + ((k * 2048) >> 4), idp, acc || k > 0);
+                mma_ts_w(tO, tS + 8 * k, db + ((k * 2048) >> 4), idp, acc || k > 0);
         };
         auto wait = [&](int i, int parity) {
-            return __all_sync(~0u, mbar_wait(bar(i), parity, abort_flag, a.status));
+            return __all_sync(~0u, mbar_wait_lazy(bar(i), parity, abort_flag, a.status));
         };
         bool ok = true;
-        int gt = 0, g1 = 0, n = 0;       // key tiles so far, those of Q tile 1, segments
+        int gt = 0, gq = 0, n = 0;       // key tiles so far, those of this Q tile, segments
         for (;; ++n) {
             const int slot = n & 1;
             if (!(ok = wait(C_L + slot, (n >> 1) & 1))) break;
             const int T = segs[slot].tb - segs[slot].ta;
-            const bool two = segs[slot].nq == 2;
+            const bool mine = q < segs[slot].nq;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C_LF + slot));
             if (T == 0) break;
+            if (!mine) {
+                // no rows here: only the arrivals that the stages count on
+                // (each after the phase before has ended)
+                if (!(ok = wait(C_Q, n & 1))) break;
+                if (lane == 0) mbar_arrive(bar(C_QFREE));
+                for (int t = 0; ok && t < T; ++t, ++gt) {
+                    if (!(ok = wait(C_KF + gt % kStages, (gt / kStages) & 1))) break;
+                    if (lane == 0) mbar_arrive(bar(C_KE + gt % kStages));
+                    if (!(ok = wait(C_VF + gt % kStages, (gt / kStages) & 1))) break;
+                    if (lane == 0) mbar_arrive(bar(C_VE + gt % kStages));
+                }
+                if (!ok) break;
+                continue;
+            }
             if (!(ok = wait(C_Q, n & 1))) break;
             if (!(ok = wait(C_KF + gt % kStages, (gt / kStages) & 1))) break;
             tc_fence_after();
-            qk(0, gt);
-            if (two) qk(1, gt);
-            mma_commit_w(bar(C_KE + gt % kStages));
+            qk(gt);
             if (T == 1) mma_commit_w(bar(C_QFREE));
-            for (int t = 0; ok && t < T; ++t) {
-                const int gg = gt + t;
-                for (int h = 0; ok && h < 4; ++h) {
-                    if (!(ok = wait(C_P + h, gg & 1))) break;
-                    if (h == 0 && !(ok = wait(C_VF + gg % kStages, (gg / kStages) & 1))) break;
+            for (int t = 0; t < T; ++t, ++gt, ++gq) {
+                if (!(ok = wait(C_VF + gt % kStages, (gt / kStages) & 1))) break;
+                for (int h = 0; h < 4; ++h) {
+                    if (!(ok = wait(C_P + 4 * q + h, gq & 1))) break;
                     tc_fence_after();
-                    pv(0, gg, h, t > 0 || h > 0);
+                    pv(gt, h, t > 0 || h > 0);
                 }
                 if (!ok) break;
-                if (!two) mma_commit_w(bar(C_VE + gg % kStages));
-                if (t == T - 1) mma_commit_w(bar(C_OD));
-                if (t + 1 < T) {
-                    if (!(ok = wait(C_KF + (gg + 1) % kStages, ((gg + 1) / kStages) & 1))) break;
+                mma_commit_w(bar(C_VE + gt % kStages));
+                if (t == T - 1) {
+                    mma_commit_w(bar(C_OD + q));
+                } else {
+                    if (!(ok = wait(C_KF + (gt + 1) % kStages, ((gt + 1) / kStages) & 1))) break;
                     tc_fence_after();
-                    qk(0, gg + 1);
-                    if (!two) {
-                        mma_commit_w(bar(C_KE + (gg + 1) % kStages));
-                        if (t + 2 == T) mma_commit_w(bar(C_QFREE));
-                    }
-                }
-                if (two) {
-                    for (int h = 0; ok && h < 4; ++h) {
-                        if (!(ok = wait(C_P + 4 + h, (g1 + t) & 1))) break;
-                        tc_fence_after();
-                        pv(1, gg, h, t > 0 || h > 0);
-                    }
-                    if (!ok) break;
-                    mma_commit_w(bar(C_VE + gg % kStages));
-                    if (t == T - 1) mma_commit_w(bar(C_OD + 1));
-                    if (t + 1 < T) {
-                        qk(1, gg + 1);
-                        mma_commit_w(bar(C_KE + (gg + 1) % kStages));
-                        if (t + 2 == T) mma_commit_w(bar(C_QFREE));
-                    }
+                    qk(gt + 1);
+                    if (t == T - 2) mma_commit_w(bar(C_QFREE));
                 }
             }
             if (!ok) break;
-            gt += T;
-            if (two) g1 += T;
         }
         // every MMA issued above has completed once this arrives
-        mma_commit_w(bar(C_END));
+        mma_commit_w(bar(C_END + q));
         volatile int never = 0;
-        mbar_wait(bar(C_END), 0, &never, a.status);
-    } else if (warp < 4) {
+        mbar_wait_lazy(bar(C_END + q), 0, &never, a.status);
+    } else if (warp == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 2) {
+        {
             // ---- codes and scales of each key tile ----------------------------
             const int boxes = 128 / a.box;
             bool ok = true;
             int gt = 0, klast = -1, vlast = -1;
             for (int n = 0; ok; ++n) {
                 const int slot = n & 1;
-                ok = mbar_wait(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
+                ok = mbar_wait_lazy(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
                 if (!__all_sync(~0u, ok)) break;
                 const Seg g = segs[slot];
                 __syncwarp();
@@ -527,7 +525,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(~0u, live)) * a.box * kD;
                     const int y = (mine * s.Hkv + g.h) * s.bs + key % s.bs;
                     const uint32_t dst = sbase + raw_off<kD>() + lane * a.box * kD;
-                    if (gt >= 1) ok = mbar_wait(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
+                    if (gt >= 1) ok = mbar_wait_lazy(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
                     if (!__all_sync(~0u, ok)) { ok = false; break; }
                     if (lane < 8)
                         scales[(gt % kScaleSlots) * 8 + lane] = make_float4(f.x, f.y, log2f(f.y), 0.f);
@@ -540,7 +538,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     __syncwarp();
                     if (live) tma_load_2d(dst, &tmK, bar(C_RK), 0, y);
                     klast = gt;
-                    if (gt >= 1) ok = mbar_wait(bar(C_RVF), (gt - 1) & 1, abort_flag, a.status);
+                    if (gt >= 1) ok = mbar_wait_lazy(bar(C_RVF), (gt - 1) & 1, abort_flag, a.status);
                     if (!__all_sync(~0u, ok)) { ok = false; break; }
                     if (lane == 0) {
                         if (bytes) mbar_expect_tx(bar(C_RV), bytes);
@@ -557,8 +555,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (lane == 0 && *abort_flag) {
                 // let the copies in flight land before the CTA exits (bounded)
                 volatile int never = 0;
-                if (klast >= 0) mbar_wait(bar(C_RK), klast & 1, &never, a.status);
-                if (vlast >= 0) mbar_wait(bar(C_RV), vlast & 1, &never, a.status);
+                if (klast >= 0) mbar_wait_lazy(bar(C_RK), klast & 1, &never, a.status);
+                if (vlast >= 0) mbar_wait_lazy(bar(C_RV), vlast & 1, &never, a.status);
             }
         }
     } else if (warp < 8) {
@@ -613,7 +611,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             __syncwarp();
         };
         auto wait = [&](int i, int parity) {
-            return __all_sync(~0u, mbar_wait(bar(i), parity, abort_flag, a.status));
+            return __all_sync(~0u, mbar_wait_lazy(bar(i), parity, abort_flag, a.status));
         };
         for (int n = 0; ok; ++n) {
             const int slot = n & 1;
@@ -645,7 +643,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         int gt = 0, gp = 0, done = 0;      // key tiles so far, this Q tile's, its segments
         for (int n = 0; ok; ++n) {
             const int slot = n & 1;
-            ok = mbar_wait(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
+            ok = mbar_wait_lazy(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
             if (!__all_sync(~0u, ok)) break;
             const Seg &g = segs[slot];      // released at the segment's end
             const int T = g.tb - g.ta;
@@ -664,8 +662,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             const float qf = row_ok ? a.qf[row] : 0.f;
             float m_run = -CUDART_INF_F, mv_run = -CUDART_INF_F, l = 0.f;   // references of l and of O
             for (int t = 0; t < T; ++t, ++gt, ++gp, vis -= 128) {
-                ok = mbar_wait(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status) &&
-                     mbar_wait(bar(C_S + q), gp & 1, abort_flag, a.status);
+                ok = mbar_wait_lazy(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status) &&
+                     mbar_wait_lazy(bar(C_S + q), gp & 1, abort_flag, a.status);
                 if (!__all_sync(~0u, ok)) { ok = false; break; }
                 tc_fence_after();
                 float x[128];
@@ -678,21 +676,21 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
                     for (int k = 0; k < 128; ++k) x[k] = k < vis ? x[k] : -CUDART_INF_F;
                 }
-                // 16 keys share a page, so a scale: the largest logit of each group
-                float mx = -CUDART_INF_F, mv = -CUDART_INF_F;
+                // 16 keys share a page, so a scale: the largest logit of each
+                // group (eight chains side by side)
+                float mx = -CUDART_INF_F, mv = -CUDART_INF_F, gm[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gm[i] = fmaxf(x[16 * i], x[16 * i + 1]);
+#pragma unroll
+                for (int k = 2; k < 16; k += 2)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) gm[i] = fmax3(gm[i], x[16 * i + k], x[16 * i + k + 1]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float m0 = fmax3(x[16 * i], x[16 * i + 1], x[16 * i + 2]);
-                    float m1 = fmax3(x[16 * i + 3], x[16 * i + 4], x[16 * i + 5]);
-                    m0 = fmax3(m0, x[16 * i + 6], x[16 * i + 7]);
-                    m1 = fmax3(m1, x[16 * i + 8], x[16 * i + 9]);
-                    m0 = fmax3(m0, x[16 * i + 10], x[16 * i + 11]);
-                    m1 = fmax3(m1, x[16 * i + 12], x[16 * i + 13]);
-                    m0 = fmax3(m0, x[16 * i + 14], x[16 * i + 15]);
                     const float4 f = sc[i];
-                    const float z = fmaxf(m0, m1) * logit_scale(f.x, qf);
-                    mx = fmaxf(mx, z);
-                    mv = fmaxf(mv, z + f.z);
+                    gm[i] *= logit_scale(f.x, qf);
+                    mx = fmaxf(mx, gm[i]);
+                    mv = fmaxf(mv, gm[i] + f.z);
                 }
                 if (t == 0) {
                     m_run = mx;
@@ -749,17 +747,25 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                             pk[8 * i + k] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
                     }
+                    // a quarter is handed over once the next one is computed,
+                    // so that its store is not waited for
+                    if (c > 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C_P + 4 * q + c - 1));
+                    }
                     tmem_st16(tS + 16 * c, pk);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C_P + 4 * q + c));
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C_P + 4 * q + 3));
                 l += (la.x + la.y) + (lb.x + lb.y);
             }
             if (!ok) break;
             // ---- epilogue ------------------------------------------------------
-            ok = mbar_wait(bar(C_OD + q), done & 1, abort_flag, a.status);
+            ok = mbar_wait_lazy(bar(C_OD + q), done & 1, abort_flag, a.status);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             ++done;
             tc_fence_after();
