@@ -22,6 +22,9 @@
 //     and m' its largest logit + log2 vs, l sums p = 2^(z - m) and the tensor
 //     core gets p vs 2^(m - m'), at most 2^8 (references are raised when a
 //     logit passes them by 2^8), whatever the scales;
+//   * S of a key tile comes in two halves of 64 keys with a buffer each, so
+//     the tensor core fills one while the softmax empties the other (one S of
+//     128 keys left the softmax waiting 30 % of the time);
 //   * the work is one line of (unit, key tile) steps cut into one equal range
 //     per CTA, whatever the lengths: a few queries over a long cache spread
 //     over every SM, and a causal triangle is balanced.  Units that ranges
@@ -32,7 +35,7 @@
 // both would hold one tile's products back while it waits, quarter by quarter,
 // for the other's weights: 3.39 against ... ms for the 4K chunk at 32K), 2
 // loads codes and scales; 4-7 convert; 8-11 and 12-15 softmax.
-// Registers: launched at 128; 56 + 88 + 2 * 184 = 4 * 128.
+// Registers: launched at 128; 112 + 112 + 2 * 144 = 4 * 128.
 // Every wait is bounded; when one runs out the CTA sets the status word, lets
 // its copies land, frees tensor memory and exits.
 #include <math_constants.h>
@@ -48,7 +51,7 @@ using namespace tc;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 512;
-constexpr int kRegsLaunch = 128, kRegsIssue = 48, kRegsConv = 64, kRegsSoft = 200;
+constexpr int kRegsLaunch = 128, kRegsIssue = 112, kRegsConv = 112, kRegsSoft = 144;
 static_assert(128 * (kRegsIssue + kRegsConv + 2 * kRegsSoft) <= kThreads * kRegsLaunch, "register split");
 constexpr int kMaxGrid = 148;
 constexpr int kMinRange = 2;                 // key tiles: a shorter range is mostly fill and drain
@@ -248,9 +251,10 @@ enum {
     C_VF = C_KF + kStages,       // [2]
     C_KE = C_VF + kStages,       // [2] K stage free, 2 arrivals (one per Q tile)
     C_VE = C_KE + kStages,
-    C_S = C_VE + kStages,        // [2 Q tiles] S ready
-    C_P = C_S + 2,               // [2 Q tiles][4 quarters] P written, 4 arrivals
-    C_OD = C_P + 8,              // [2 Q tiles] last PV of the segment done
+    C_S = C_VE + kStages,        // [2 Q tiles][2 halves] S of 64 keys ready
+    C_P = C_S + 4,               // [2 Q tiles][2 halves][2] P of 32 keys written, 4 arrivals
+    C_PV = C_P + 8,              // [2 Q tiles] PV of a half done
+    C_OD = C_PV + 2,             // [2 Q tiles] last PV of the segment done
     C_L = C_OD + 2,              // [2] segment described
     C_LF = C_L + 2,              // [2] segment released, 15 arrivals
     C_SC = C_LF + 2,             // [4] scales of a key tile written
@@ -406,26 +410,27 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         // ---- MMA issuers: Q tile 0 and Q tile 1 --------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));     // the operand formats' bits: fp16 instead of bf16
-        constexpr uint32_t idq = idesc_bf16(false, 128) & kFp16, idp = idesc_bf16(true, kD) & kFp16;
+        constexpr uint32_t idq = idesc_bf16(false, 64) & kFp16, idp = idesc_bf16(true, kD) & kFp16;
         const int q = warp >> 1;
         const uint32_t tS = tmem + q * 128, tO = tmem + 256 + q * 128;
         const uint64_t dq = desc_k_sw128(sbase + q * kTile);
-        auto qk = [&](int gg) {
-            const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile);
+        // S of half h of key tile gg (64 keys)
+        auto qk = [&](int gg, int h) {
+            const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile + h * 8192);
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
                 const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-                mma_ss_w(tS, dq + off, db + off, idq, k > 0);
+                mma_ss_w(tS + 64 * h, dq + off, db + off, idq, k > 0);
             }
-            mma_commit_w(bar(C_S + q));
-            mma_commit_w(bar(C_KE + gg % kStages));
+            mma_commit_w(bar(C_S + 2 * q + h));
+            if (h == 1) mma_commit_w(bar(C_KE + gg % kStages));
         };
-        // O += P V for keys 32 h .. 32 h + 31; P (fp16) is the first 64 columns of S
-        auto pv = [&](int gg, int h, bool acc) {
+        // O += P V for 32 keys (e of half h); P (fp16) is the first 32 columns of its S
+        auto pv = [&](int gg, int h, int e, bool acc) {
             const uint64_t db = desc_mn_sw128(sbase + v_off<kD>() + (gg % kStages) * kTile, kChunk);
 #pragma unroll
-            for (int k = 2 * h; k < 2 * h + 2; ++k)
-                mma_ts_w(tO, tS + 8 * k, db + ((k * 2048) >> 4), idp, acc || k > 0);
+            for (int k = 2 * e; k < 2 * e + 2; ++k)
+                mma_ts_w(tO, tS + 64 * h + 8 * k, db + (((4 * h + k) * 2048) >> 4), idp, acc || k > 0);
         };
         auto wait = [&](int i, int parity) {
             return __all_sync(~0u, mbar_wait_lazy(bar(i), parity, abort_flag, a.status));
@@ -457,24 +462,28 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!(ok = wait(C_Q, n & 1))) break;
             if (!(ok = wait(C_KF + gt % kStages, (gt / kStages) & 1))) break;
             tc_fence_after();
-            qk(gt);
+            qk(gt, 0);
+            qk(gt, 1);
             if (T == 1) mma_commit_w(bar(C_QFREE));
-            for (int t = 0; t < T; ++t, ++gt, ++gq) {
+            for (int t = 0; ok && t < T; ++t, ++gt, ++gq) {
                 if (!(ok = wait(C_VF + gt % kStages, (gt / kStages) & 1))) break;
-                for (int h = 0; h < 4; ++h) {
-                    if (!(ok = wait(C_P + 4 * q + h, gq & 1))) break;
-                    tc_fence_after();
-                    pv(gt, h, t > 0 || h > 0);
-                }
-                if (!ok) break;
-                mma_commit_w(bar(C_VE + gt % kStages));
-                if (t == T - 1) {
-                    mma_commit_w(bar(C_OD + q));
-                } else {
-                    if (!(ok = wait(C_KF + (gt + 1) % kStages, ((gt + 1) / kStages) & 1))) break;
-                    tc_fence_after();
-                    qk(gt + 1);
-                    if (t == T - 2) mma_commit_w(bar(C_QFREE));
+                for (int h = 0; h < 2; ++h) {
+                    for (int e = 0; e < 2; ++e) {
+                        if (!(ok = wait(C_P + 4 * q + 2 * h + e, gq & 1))) break;
+                        tc_fence_after();
+                        pv(gt, h, e, t > 0 || h > 0 || e > 0);
+                    }
+                    if (!ok) break;
+                    mma_commit_w(bar(C_PV + q));
+                    if (h == 1) mma_commit_w(bar(C_VE + gt % kStages));
+                    if (h == 1 && t + 1 == T) mma_commit_w(bar(C_OD + q));
+                    if (t + 1 < T) {
+                        // the next tile's half, in the place of the one just used up
+                        if (h == 0 && !(ok = wait(C_KF + (gt + 1) % kStages, ((gt + 1) / kStages) & 1))) break;
+                        tc_fence_after();
+                        qk(gt + 1, h);
+                        if (h == 1 && t + 2 == T) mma_commit_w(bar(C_QFREE));
+                    }
                 }
             }
             if (!ok) break;
@@ -656,49 +665,48 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             }
             const int tok = q * a.tpt + tok_r;
             const bool row_ok = tok_r < a.tpt && tok < g.ntok;
-            // keys the row sees, from the segment's first tile on
+            // keys the row sees, from the half tile at hand on
             int vis = (s.flags & SA_CAUSAL ? max(0, min(g.n, g.pos0 + tok + 1)) : g.n) - 128 * g.ta;
             const size_t row = row_ok ? (size_t)(g.row0 + tok) * s.Hq + g.h * s.G + head_r : 0;
             const float qf = row_ok ? a.qf[row] : 0.f;
             float m_run = -CUDART_INF_F, mv_run = -CUDART_INF_F, l = 0.f;   // references of l and of O
-            for (int t = 0; t < T; ++t, ++gt, ++gp, vis -= 128) {
-                ok = mbar_wait_lazy(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status) &&
-                     mbar_wait_lazy(bar(C_S + q), gp & 1, abort_flag, a.status);
-                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                tc_fence_after();
-                float x[128];
+            for (int t = 0; t < T; ++t, ++gt, ++gp) {
+                ok = mbar_wait_lazy(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status);
+                for (int h = 0; h < 2; ++h, vis -= 64) {
+                    ok = ok && mbar_wait_lazy(bar(C_S + 2 * q + h), gp & 1, abort_flag, a.status);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
+                    tc_fence_after();
+                    float x[64];
+                    tmem_ld32(tS + 64 * h, x);
+                    tmem_ld32(tS + 64 * h + 32, x + 32);
+                    tmem_wait_ld();
+                    reg_fence<64>(x);
+                    if (vis < 64) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
-                tmem_wait_ld();
-                reg_fence<128>(x);
-                const float4 *sc = scales + (gt % kScaleSlots) * 8;
-                if (vis < 128) {
+                        for (int k = 0; k < 64; ++k) x[k] = k < vis ? x[k] : -CUDART_INF_F;
+                    }
+                    // 16 keys share a page, so a scale: the largest logit of each
+                    // group (four chains side by side)
+                    const float4 *sc = scales + (gt % kScaleSlots) * 8 + 4 * h;
+                    float gm[4], sk[4], lv[4];
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) x[k] = k < vis ? x[k] : -CUDART_INF_F;
-                }
-                // 16 keys share a page, so a scale: the largest logit of each
-                // group (eight chains side by side)
-                float mx = -CUDART_INF_F, mv = -CUDART_INF_F, gm[8];
+                    for (int i = 0; i < 4; ++i) gm[i] = fmaxf(x[16 * i], x[16 * i + 1]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) gm[i] = fmaxf(x[16 * i], x[16 * i + 1]);
+                    for (int k = 2; k < 16; k += 2)
 #pragma unroll
-                for (int k = 2; k < 16; k += 2)
+                        for (int i = 0; i < 4; ++i) gm[i] = fmax3(gm[i], x[16 * i + k], x[16 * i + k + 1]);
+                    float mx = -CUDART_INF_F, mv = -CUDART_INF_F;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) gm[i] = fmax3(gm[i], x[16 * i + k], x[16 * i + k + 1]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 f = sc[i];
-                    gm[i] *= logit_scale(f.x, qf);
-                    mx = fmaxf(mx, gm[i]);
-                    mv = fmaxf(mv, gm[i] + f.z);
-                }
-                if (t == 0) {
-                    m_run = mx;
-                    mv_run = mv;
-                } else {
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = sc[i];
+                        sk[i] = logit_scale(f.x, qf);
+                        lv[i] = f.z;
+                        gm[i] *= sk[i];
+                        mx = fmaxf(mx, gm[i]);
+                        mv = fmaxf(mv, gm[i] + lv[i]);
+                    }
                     const bool need = mx > m_run + 8.f || mv > mv_run + 8.f;
                     if (__any_sync(~0u, need)) {
-                        // the PV before this S has completed: O is stable
                         float corr = 1.f;
                         if (need) {
                             const float m1 = fmaxf(mx, m_run), v1 = fmaxf(mv, mv_run);
@@ -707,61 +715,69 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                             m_run = m1;
                             mv_run = v1;
                         }
+                        if (t > 0 || h > 0) {
+                            // O is stable once the product of the half before
+                            // is done (S ready: the one before that is; this
+                            // half's waits for the weights below)
+                            ok = mbar_wait_lazy(bar(C_PV + q), (2 * gp + h - 1) & 1, abort_flag, a.status);
+                            if (!__all_sync(~0u, ok)) { ok = false; break; }
+                            tc_fence_after();
 #pragma unroll
-                        for (int cc = 0; cc < kD / 32; ++cc) {
-                            float o[32];
-                            tmem_ld32(tO + 32 * cc, o);
-                            tmem_wait_ld();
-                            reg_fence<32>(o);
+                            for (int cc = 0; cc < kD / 8; ++cc) {
+                                float o[8];
+                                tmem_ld8(tO + 8 * cc, o);
+                                tmem_wait_ld();
+                                reg_fence<8>(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= corr;
-                            tmem_st32(tO + 32 * cc, reinterpret_cast<const uint32_t *>(o));
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                const float ref = m_run == -CUDART_INF_F ? 0.f : m_run;
-                const float2 b2 = make_float2(-ref, -ref);
-                // p vs 2^(m - m'); the limit keeps the factor of keys whose p
-                // is 0 finite
-                const float vf = mv_run == -CUDART_INF_F ? 0.f : ref - mv_run;
-                float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 f = sc[2 * c + i];
-                        const float v = ex2(fminf(f.z + vf, 126.f));
-                        const float k1 = logit_scale(f.x, qf);
-                        const float2 sk = make_float2(k1, k1), sv = make_float2(v, v);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int e = 32 * c + 16 * i + 2 * k;
-                            const float2 z = ffma2(make_float2(x[e], x[e + 1]), sk, b2);
-                            float2 p = make_float2(ex2(z.x), ex2(z.y));
-                            if (k & 1) lb = fadd2(lb, p);
-                            else la = fadd2(la, p);
-                            p = fmul2(p, sv);
-                            const __half2 h2 = __floats2half2_rn(p.x, p.y);
-                            pk[8 * i + k] = *reinterpret_cast<const uint32_t *>(&h2);
+                                for (int k = 0; k < 8; ++k) o[k] *= corr;
+                                tmem_st8(tO + 8 * cc, reinterpret_cast<const uint32_t *>(o));
+                            }
+                            tmem_wait_st();
                         }
                     }
-                    // a quarter is handed over once the next one is computed,
-                    // so that its store is not waited for
-                    if (c > 0) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C_P + 4 * q + c - 1));
+                    // w = p vs 2^(m - m') = 2^(z - m + e), e = log2 vs + m - m'
+                    // of the group: one exponential a key; l gets the group's
+                    // sum times 2^-e.  The limits on e keep 2^-e and the
+                    // exponential finite; at vs = 0 (e = -100) w vanishes in
+                    // fp16 and l loses only what is under 2^-26 of the row.
+                    const float ref = m_run == -CUDART_INF_F ? 0.f : m_run;
+                    const float vf = mv_run == -CUDART_INF_F ? 0.f : ref - mv_run;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float ex = fmaxf(fminf(lv[2 * e + i] + vf, 100.f), -100.f);
+                            const float2 f2 = make_float2(sk[2 * e + i], sk[2 * e + i]), b2 = make_float2(ex - ref, ex - ref);
+                            float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int c = 32 * e + 16 * i + 2 * k;
+                                const float2 z = ffma2(make_float2(x[c], x[c + 1]), f2, b2);
+                                const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                                if (k & 1) lb = fadd2(lb, p);
+                                else la = fadd2(la, p);
+                                const __half2 h2 = __floats2half2_rn(p.x, p.y);
+                                pk[8 * i + k] = *reinterpret_cast<const uint32_t *>(&h2);
+                            }
+                            l = fmaf((la.x + la.y) + (lb.x + lb.y), ex2(-ex), l);
+                        }
+                        // the first 32 keys are handed over once the others are
+                        // computed, so that their store is not waited for
+                        if (e == 1) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(C_P + 4 * q + 2 * h));
+                        }
+                        tmem_st16(tS + 64 * h + 16 * e, pk);
                     }
-                    tmem_st16(tS + 16 * c, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C_P + 4 * q + 2 * h + 1));
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C_P + 4 * q + 3));
-                l += (la.x + la.y) + (lb.x + lb.y);
+                if (!ok) break;
             }
             if (!ok) break;
             // ---- epilogue ------------------------------------------------------
