@@ -22,7 +22,8 @@ namespace {
 constexpr int kTabThreads = 512;
 
 struct Sum3 {
-    int t, a, r;   // new tokens, pages wanted, pages released
+    long long t;   // new tokens (a call whose sum passes 32 bits is refused)
+    int a, r;      // pages wanted, pages released
 };
 __device__ __forceinline__ Sum3 add3(Sum3 x, Sum3 y) { return {x.t + y.t, x.a + y.a, x.r + y.r}; }
 
@@ -46,17 +47,12 @@ paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t
     int *offT = sm_tab, *offA = offT + B + 1, *offR = offA + B + 1;
     __shared__ Sum3 wsum[kTabThreads / 32];
     __shared__ int bad_s;
-    __shared__ long long big_s;
-    if (tid == 0) {
-        bad_s = 0;
-        big_s = 0;
-    }
+    if (tid == 0) bad_s = 0;
     __syncthreads();
     const int per = (B + kTabThreads - 1) / kTabThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     const int most = s.maxb * bs;
     Sum3 mine{0, 0, 0};
-    long long tok = 0;   // the sum of new tokens may pass 32 bits; such a call is refused
     int bad = 0;
     for (int b = b0; b < b1; ++b) {
         const int c = cur[b], w = want[b];
@@ -65,11 +61,9 @@ paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t
             continue;
         }
         const int oc = (c + bs - 1) / bs, ow = (w + bs - 1) / bs;
-        tok += max(0, w - c);
         mine = add3(mine, {max(0, w - c), max(0, ow - oc), max(0, oc - ow)});
     }
     if (bad) bad_s = 1;
-    if (tok) atomicAdd(reinterpret_cast<unsigned long long *>(&big_s), (unsigned long long)tok);
     Sum3 inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -86,17 +80,17 @@ paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t
     Sum3 at = add3(base, {inc.t - mine.t, inc.a - mine.a, inc.r - mine.r});
     const int nf = n_free_in[0];
     const bool wrong = bad_s || nf < 0 || nf > s.pages;
-    const bool out = !wrong && (big_s > s.tokens || tot.a > (long long)nf + tot.r || nf + (long long)tot.r - tot.a > s.pages);
+    const bool out = !wrong && (tot.t > s.tokens || tot.a > (long long)nf + tot.r || nf + (long long)tot.r - tot.a > s.pages);
     const bool refuse = wrong || out;   // nothing changes: no slots, the same free pages
     for (int b = b0; b < b1; ++b) {
         const int c = refuse ? 0 : cur[b], w = refuse ? 0 : want[b];
         const int oc = (c + bs - 1) / bs, ow = (w + bs - 1) / bs;
-        offT[b] = refuse ? 0 : at.t;
+        offT[b] = refuse ? 0 : (int)at.t;
         offA[b] = refuse ? 0 : at.a;
         offR[b] = refuse ? 0 : at.r;
         at = add3(at, {max(0, w - c), max(0, ow - oc), max(0, oc - ow)});
     }
-    const int T = refuse ? 0 : tot.t, A = refuse ? 0 : tot.a, R = refuse ? 0 : tot.r;
+    const int T = refuse ? 0 : (int)tot.t, A = refuse ? 0 : tot.a, R = refuse ? 0 : tot.r;
     if (tid == 0) {
         offT[B] = T;
         offA[B] = A;

@@ -41,10 +41,12 @@ using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 6;      // ranges per CTA
-constexpr int kRing = 2;       // stages per warp
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMinRange = 4;   // stages: shorter ranges cost more in records than they save
+// Ranges (warps) per CTA: one stage of 64 keys each (16 KB at d = 128) fills
+// shared memory at 12; two head tiles need more registers than 12 warps have.
+template <int kNT>
+constexpr int warps_of() { return kNT == 1 ? 12 : 8; }
+constexpr int kMaxWarps = 12;
+constexpr int kMinRange = 2;   // stages: shorter ranges cost more in records than they save
 constexpr int kMergeWarps = 8;
 // stage flags: first / last stage of its unit in this range, the unit lies in
 // this range as a whole, it begins before this range, some keys are not there
@@ -65,10 +67,10 @@ struct DecArgs {
     int tiles;           // 16-key tiles per stage
 };
 
-// One ring stage's record for its consumer.
-struct __align__(16) Meta {
-    float4 tile[4];      // per 16 keys: key scale, value scale, gate (or score), valid keys
-    int unit, flags, pad[2];
+// A part's record for the stage that reads it.
+struct __align__(16) Part {
+    float ks, vs, gate;   // key scale, value scale, gate (hierarchical: score), log2 units
+    int nk;               // valid keys (0: not loaded)
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
@@ -81,14 +83,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
 }
 __device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
@@ -236,27 +238,30 @@ struct Acc {
     }
 };
 
-// What a warp knows of the stages it issues next: up to 32 parts of one unit,
-// one per lane, loaded in steps so that the chain count -> list -> table ->
-// scales is in flight behind the stages before it.
+// What a warp loads next: up to 32 parts of one unit, one per lane, in steps
+// so that the chain count -> list -> table -> scales is in flight behind the
+// stages before it.
 struct Batch {
     int unit, entries;          // -1: none
     int s0, s1;                 // stages of the unit
     int flags;                  // F_NEW: s0 is the unit's first stage here; F_LAST: s1 - 1 its last; F_WHOLE, F_CUT
     int step;                   // load steps done
-    int blk, page, nk;          // lane: block (-1: none), page, valid keys of its part
-    float ks, vs, gate;
+    int page;                   // lane: block, then page of its part (-1: none)
+    int nk;                     // lane: valid keys
+    float gate;
 };
 
 template <int kD, int kCode, int kNT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * warps_of<kNT>(), 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecArgs a) {
     constexpr uint32_t kHalfBytes = 64 * kD;
+    constexpr int kWarps = warps_of<kNT>(), kThreads = 32 * kWarps;
     extern __shared__ unsigned char dec_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dec_raw) + 1023) &
                                                           ~uintptr_t(1023));
-    __shared__ Meta meta[kWarps][kRing];
-    __shared__ uint64_t bars[kWarps][kRing];
+    __shared__ Part parts[kWarps][2][32];     // of two batches
+    __shared__ int part_y[kWarps][32];        // first cache row of the batch being issued
+    __shared__ uint64_t bars[kWarps][2];      // the warp's keys, its values
     __shared__ long long pre[kThreads + 1];
     __shared__ long long wtot[kWarps];
     __shared__ volatile int abort_s;
@@ -264,7 +269,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const bool hier = s.flags & SA_HIER;
     if (tid == 0) {
-        for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+        for (int i = 0; i < kWarps * 2; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
         abort_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -313,6 +318,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (x0 >= x1) return;
 
     // ---- issue side ----------------------------------------------------------
+    int batch = 1;                     // batches issued (records alternate between two places)
     int bu;                            // unit of stage xi, and its first stage
     long long bpu, xi = x0;            // xi: next stage to put in a batch
     {
@@ -354,114 +360,123 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const UnitAt w = unit_at<kNT>(a, t.unit);
         if (t.step == 1) {
             const int c = t.s0 * a.pps + lane, e = c / a.sub;
-            t.blk = -1;
+            t.page = -1;
             t.gate = 0.f;
             t.nk = 0;
             if (lane < (t.s1 - t.s0) * a.pps && e < t.entries) {
                 const int n = paged_len(s, a.c.seq_len, w.b), local = (n + s.bs - 1) / s.bs - 1;
-                t.blk = e;
+                int blk = e;
                 if (a.l.idx) {
                     const int32_t *il = a.l.idx + w.lu * s.cap;
                     const float *sc = a.l.score + w.lu * s.cap;
                     const int before = e > 0 ? il[e - 1] : -1;
                     const float mine = sc[e], loc = sc[t.entries - 1];
-                    t.blk = il[e];
-                    if (t.blk <= before || t.blk < 0 || t.blk > local) {
+                    blk = il[e];
+                    if (blk <= before || blk < 0 || blk > local) {
                         set_status(a.status, kStatusBadIndex);
-                        t.blk = -1;
+                        blk = -1;
                     }
-                    const bool forced = (t.blk == local && (s.flags & SA_LOCAL)) || (t.blk == 0 && (s.flags & SA_SINK));
+                    const bool forced = (blk == local && (s.flags & SA_LOCAL)) || (blk == 0 && (s.flags & SA_SINK));
                     t.gate = hier ? mine * kLog2e
                                   : ((s.flags & SA_GATE) && !forced ? log_sigmoid(mine - loc) * kLog2e : 0.f);
                 }
                 const int row0 = (c - e * a.sub) * a.rows;
-                t.nk = min(min(a.rows, s.bs - row0), n - t.blk * s.bs - row0);
-                if (t.nk <= 0) t.blk = -1;
+                t.nk = min(min(a.rows, s.bs - row0), n - blk * s.bs - row0);
+                if (t.nk > 0) t.page = blk;
             }
         } else if (t.step == 2) {
-            t.page = t.blk >= 0 ? a.c.table[(size_t)w.b * s.maxb + t.blk] : -1;
-        } else {
-            if (t.blk >= 0 && (t.page < 0 || t.page >= s.pages)) {
-                set_status(a.status, kStatusBadIndex);
-                t.page = -1;
-            }
-            t.ks = t.vs = 0.f;
             if (t.page >= 0) {
-                const size_t ph = (size_t)t.page * s.Hkv + w.g;
-                t.ks = a.c.ks[ph];
-                t.vs = a.c.vs[ph];
+                t.page = a.c.table[(size_t)w.b * s.maxb + t.page];
+                if (t.page < 0 || t.page >= s.pages) {
+                    set_status(a.status, kStatusBadIndex);
+                    t.page = -1;
+                }
             }
+        } else {
+            // the records go where the batch before the last one had its own
+            Part p{0.f, 0.f, t.gate, 0};
+            int y = 0;
+            if (t.page >= 0) {
+                const int ph = t.page * s.Hkv + w.g;
+                p.ks = a.c.ks[ph];
+                p.vs = a.c.vs[ph];
+                p.nk = t.nk;
+                y = ph * s.bs + (t.s0 * a.pps + lane) % a.sub * a.rows;
+            }
+            parts[warp][batch & 1][lane] = p;
+            part_y[warp][lane] = y;
+            __syncwarp();
         }
         ++t.step;
     };
-    Batch cur, nxt;
-    open(cur);
-    while (cur.step < 4) more(cur);
-    open(nxt);
-    int ci = 0;                        // stages of cur already issued
-    const uint32_t ring = smem_u32(sm) + warp * kRing * 2 * kHalfBytes;
-    const uint32_t bar0 = smem_u32(&bars[warp][0]);
+    // The batch being issued (its records are in shared memory) and the one
+    // being loaded behind it, whose last step waits until it takes over.
+    Batch nxt;
+    int cu_unit = -1, cu_n = 0, cu_flags = 0, ci = 0;   // unit, stages, flags, stages issued
+    const uint32_t kb = smem_u32(sm) + warp * 2 * kHalfBytes, vb = kb + kHalfBytes;
+    const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
     const uint32_t part_bytes = (uint32_t)a.rows * kD;
-    // loads the range's next stage into `slot`; false when there is none
-    auto issue = [&](int slot) -> bool {
-        if (cur.unit >= 0 && ci == cur.s1 - cur.s0) {
-            while (nxt.unit >= 0 && nxt.step < 4) more(nxt);
-            cur = nxt;
+    // tile t of a stage lies in part t >> psh, as its (t & pmask)th 16 keys
+    const int psh = a.pps == 1 ? 2 : (a.rows >> 4) - 1, pmask = (1 << psh) - 1;
+    // The next stage: its keys go out once the stage at hand has made its
+    // scores, its values once that one has used its own, so one stage of
+    // memory keeps one load in flight behind the arithmetic.
+    uint32_t n_bytes = 0;
+    int n_flags = 0, n_unit = 0, n_first = 0;   // flags, unit and first part (with the batch's half) of that stage
+    auto issue_k = [&]() -> bool {              // false: the range is issued
+        if (ci == cu_n) {
+            if (nxt.unit < 0) return false;
+            ++batch;
+            while (nxt.step < 4) more(nxt);
+            cu_unit = nxt.unit;
+            cu_n = nxt.s1 - nxt.s0;
+            cu_flags = nxt.flags;
             ci = 0;
             open(nxt);
         }
-        if (cur.unit < 0) return false;
-        Meta &md = meta[warp][slot];
-        const int part = lane - ci * a.pps;
-        const bool mine = part >= 0 && part < a.pps, live = mine && cur.page >= 0;
-        const unsigned lives = __ballot_sync(~0u, live);
-        const bool tail = __any_sync(~0u, mine && (!live || cur.nk < a.rows));
-        if (mine) {
-            const int t16 = a.rows >> 4;
-            for (int t = 0; t < t16; ++t)
-                md.tile[part * t16 + t] = make_float4(cur.ks, cur.vs, cur.gate,
-                                                      __int_as_float(live ? max(0, min(16, cur.nk - 16 * t)) : 0));
-        }
-        const uint32_t bar = bar0 + 8 * slot;
+        const int first = ci * a.pps, at = first + lane;
+        const int nk = lane < a.pps ? parts[warp][batch & 1][at].nk : a.rows;
+        const unsigned lives = __ballot_sync(~0u, lane < a.pps && nk > 0);
+        n_bytes = part_bytes * __popc(lives);
+        n_first = 32 * (batch & 1) + first;
+        n_unit = cu_unit;
+        n_flags = (cu_flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cu_flags & F_NEW : 0) |
+                  (ci == cu_n - 1 ? cu_flags & F_LAST : 0) | (__any_sync(~0u, nk < a.rows) ? F_TAIL : 0);
         if (lane == 0) {
-            md.unit = cur.unit;
-            md.flags = (cur.flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cur.flags & F_NEW : 0) |
-                       (ci == cur.s1 - cur.s0 - 1 ? cur.flags & F_LAST : 0) | (tail ? F_TAIL : 0);
-            if (lives) mbar_expect_tx(bar, 2 * part_bytes * __popc(lives));
-            else mbar_arrive(bar);
+            if (n_bytes) mbar_expect_tx(bar_k, n_bytes);
+            else mbar_arrive(bar_k);
         }
         __syncwarp();
-        if (live) {
-            const int row0 = ((cur.s0 * a.pps + lane) % a.sub) * a.rows;
-            const int g = unit_at<kNT>(a, cur.unit).g;
-            const int y = (cur.page * s.Hkv + g) * s.bs + row0;
-            const uint32_t dst = ring + slot * 2 * kHalfBytes + part * part_bytes;
-            tma_load_2d(dst, &tmK, bar, 0, y);
-            tma_load_2d(dst + kHalfBytes, &tmV, bar, 0, y);
-        }
-        ++ci;
-        if (nxt.unit >= 0 && nxt.step < 4) more(nxt);
+        if (lane < a.pps && nk > 0) tma_load_2d(kb + lane * part_bytes, &tmK, bar_k, 0, part_y[warp][at]);
         return true;
     };
+    auto issue_v = [&]() {
+        if (lane == 0) {
+            if (n_bytes) mbar_expect_tx(bar_v, n_bytes);
+            else mbar_arrive(bar_v);
+        }
+        __syncwarp();
+        const int at = ci * a.pps + lane;
+        if (lane < a.pps && parts[warp][batch & 1][at].nk > 0)
+            tma_load_2d(vb + lane * part_bytes, &tmV, bar_v, 0, part_y[warp][at]);
+        ++ci;
+        if (nxt.unit >= 0 && nxt.step < 3) more(nxt);
+    };
+    open(nxt);
 
     // ---- consumer side -------------------------------------------------------
     Acc<kD, kNT> acc;
     uint32_t qb[kD / 16][kNT][2];
     float qf[2 * kNT];
-    int issued = 0, done = 0;
-    for (; issued < kRing; ++issued)
-        if (!issue(issued)) break;
-    bool ok = true;
-    for (; done < issued; ++done) {
-        const int slot = done % kRing;
-        ok = mbar_wait(bar0 + 8 * slot, (done / kRing) & 1, &abort_s, a.status);
+    int done = 0;
+    // v_out: this stage's values are on their way; k_next: the next one's keys
+    bool ok = true, have = issue_k(), v_out = have, k_next = false;
+    if (have) issue_v();
+    for (; have; ++done) {
+        ok = mbar_wait_lazy(bar_k, done & 1, &abort_s, a.status);
         if (!__all_sync(~0u, ok)) break;
-        const Meta &md = meta[warp][slot];
-        const int flags = md.flags, unit = md.unit;
-        float4 ti[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            ti[t] = t < a.tiles ? md.tile[t] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int flags = n_flags, unit = n_unit;
+        const Part *part = &parts[warp][0][n_first];
         if (flags & F_NEW) {
             // the unit's queries: dimensions 16 k + 4 tq + {0, 1}, {2, 3} of head 8 n + gq
             const UnitAt w = unit_at<kNT>(a, unit);
@@ -500,7 +515,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 }
             }
         }
-        const uint32_t kb = ring + slot * 2 * kHalfBytes, vb = kb + kHalfBytes;
         const int mrow = (lane & 7) + (lane & 8), mch = lane >> 4;   // row and chunk of the lane's ldmatrix address
         // S^T = K q^T: 16 keys x 8 heads per tile
         float z[4][kNT][4];
@@ -509,34 +523,40 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
             for (int n = 0; n < kNT; ++n) z[t][n][0] = z[t][n][1] = z[t][n][2] = z[t][n][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kD / 32; ++k)
+        for (int k = 0; k < kD / 32; ++k) {
+            uint32_t kr[4][4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t >= a.tiles) continue;
-                uint32_t r[4], p0, q0, p1, q1;
-                ldsm4(kb + swz<kD>(16 * t + mrow, 2 * k + mch), r);
-                to_h2<kCode, false>(r[0], p0, q0);
-                to_h2<kCode, false>(r[1], p1, q1);
+            for (int t = 0; t < 4; ++t)
+                if (t < a.tiles) ldsm4(kb + swz<kD>(16 * t + mrow, 2 * k + mch), kr[t]);
 #pragma unroll
-                for (int n = 0; n < kNT; ++n) mma_f16(z[t][n], p0, p1, q0, q1, qb[2 * k][n][0], qb[2 * k][n][1]);
-                to_h2<kCode, false>(r[2], p0, q0);
-                to_h2<kCode, false>(r[3], p1, q1);
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                    mma_f16(z[t][n], p0, p1, q0, q1, qb[2 * k + 1][n][0], qb[2 * k + 1][n][1]);
-            }
+                for (int t = 0; t < 4; ++t) {
+                    if (t >= a.tiles) continue;
+                    const uint32_t *r = kr[t] + 2 * half;
+                    uint32_t p0, q0, p1, q1;
+                    to_h2<kCode, false>(r[0], p0, q0);
+                    to_h2<kCode, false>(r[1], p1, q1);
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+                        mma_f16(z[t][n], p0, p1, q0, q1, qb[2 * k + half][n][0], qb[2 * k + half][n][1]);
+                }
+        }
+        __syncwarp();
+        k_next = issue_k();
         // logits in log2 units, -inf where there is no key
         float top[2 * kNT];
 #pragma unroll
         for (int i = 0; i < 2 * kNT; ++i) top[i] = -CUDART_INF_F;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int nk = t < a.tiles ? __float_as_int(ti[t].w) : 0;
+            const Part pt = part[t >> psh];
+            const int nk = t < a.tiles ? pt.nk - 16 * (t & pmask) : 0;
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = fmaf(z[t][n][e], qf[2 * n + (e & 1)] * ti[t].x, hier ? 0.f : ti[t].z);
+                    const float x = fmaf(z[t][n][e], qf[2 * n + (e & 1)] * pt.ks, hier ? 0.f : pt.gate);
                     z[t][n][e] = gq + 8 * (e >> 1) < nk ? x : -CUDART_INF_F;
                     top[2 * n + (e & 1)] = fmaxf(top[2 * n + (e & 1)], z[t][n][e]);
                 }
@@ -586,6 +606,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     sum[i] += p;
                 }
         if (hier) {
+            const float score = part[0].gate;
             float f[2 * kNT];
 #pragma unroll
             for (int i = 0; i < 2 * kNT; ++i) {
@@ -596,9 +617,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 f[i] = 1.f;
                 pf[i] = 0.f;
                 if (lb > 0.f) {
-                    const float M = fmaxf(acc.m[i], ti[0].z);
+                    const float M = fmaxf(acc.m[i], score);
                     f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - M);
-                    const float w = ex2(ti[0].z - M);
+                    const float w = ex2(score - M);
                     acc.m[i] = M;
                     // the sum over lanes at the end counts it once
                     acc.l[i] = acc.l[i] * f[i] + (gq == 0 ? w : 0.f);
@@ -621,10 +642,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 pb[t][n][1] = transpose8(pack_h2(z[t][n][2] * f0, z[t][n][3] * f1));
             }
         // O^T += V^T P^T, 32 dimensions at a time
+        ok = mbar_wait_lazy(bar_v, done & 1, &abort_s, a.status);
+        if (!__all_sync(~0u, ok)) break;
         const bool one_page = a.pps == 1;
+        const float vs0 = part[0].vs;
         const bool blank = kCode == SA_E4M3 && (flags & F_TAIL);   // what is not a key may hold NaN codes
 #pragma unroll
         for (int np = 0; np < kD / 32; ++np) {
+            uint32_t vr[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t < a.tiles) ldsm4t(vb + swz<kD>(16 * t + mrow, 2 * np + mch), vr[t]);
             float d[2][kNT][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -633,10 +661,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 if (t >= a.tiles) continue;
-                uint32_t r[4];
-                ldsm4t(vb + swz<kD>(16 * t + mrow, 2 * np + mch), r);
+                uint32_t *r = vr[t];
                 if (blank) {
-                    const int nk = __float_as_int(ti[t].w);
+                    const int nk = part[t >> psh].nk - 16 * (t & pmask);
                     const uint32_t m0 = (2 * tq < nk ? 0xffffu : 0u) | (2 * tq + 1 < nk ? 0xffff0000u : 0u);
                     const uint32_t m1 = (2 * tq + 8 < nk ? 0xffffu : 0u) | (2 * tq + 9 < nk ? 0xffff0000u : 0u);
                     r[0] &= m0;
@@ -659,7 +686,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         for (int n = 0; n < kNT; ++n)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                acc.o[2 * np + h][n][e] = fmaf(ti[t].y, d[h][n][e], acc.o[2 * np + h][n][e]);
+                                acc.o[2 * np + h][n][e] = fmaf(part[t >> psh].vs, d[h][n][e], acc.o[2 * np + h][n][e]);
                                 d[h][n][e] = 0.f;
                             }
                 }
@@ -671,11 +698,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     for (int n = 0; n < kNT; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            acc.o[2 * np + h][n][e] = fmaf(ti[0].y, d[h][n][e], acc.o[2 * np + h][n][e]);
+                            acc.o[2 * np + h][n][e] = fmaf(vs0, d[h][n][e], acc.o[2 * np + h][n][e]);
             }
         }
         __syncwarp();
-        if (issue(slot)) ++issued;
+        have = v_out = k_next;
+        k_next = false;
+        if (have) issue_v();
         if (flags & F_LAST) {
 #pragma unroll
             for (int i = 0; i < 2 * kNT; ++i) {
@@ -689,8 +718,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
     if (!ok) {
         // a wait ran out: let the copies in flight land before the CTA exits
+        // (the keys of this stage or of the next, the values of this stage)
         volatile int never = 0;
-        for (; done < issued; ++done) mbar_wait(bar0 + 8 * (done % kRing), (done / kRing) & 1, &never, a.status);
+        if (v_out) mbar_wait_lazy(bar_v, done & 1, &never, a.status);
+        mbar_wait_lazy(bar_k, done & 1, &never, a.status);
+        if (k_next) mbar_wait_lazy(bar_k, (done + 1) & 1, &never, a.status);
     }
 }
 
@@ -739,11 +771,11 @@ constexpr int kMaxGrid = 148;
 
 template <int kD, int kCode, int kNT>
 cudaError_t run(const DecArgs &a, int grid, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
-    constexpr int smem = kWarps * kRing * 2 * 64 * kD + 1024;
+    constexpr int smem = warps_of<kNT>() * 2 * 64 * kD + 1024;
     auto kern = paged_decode_kernel<kD, kCode, kNT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, mk, mv, a);
+    e = launch_pdl(kern, dim3((unsigned)grid), dim3(32 * warps_of<kNT>()), smem, st, mk, mv, a);
     note_launch();
     if (e != cudaSuccess) return e;
     e = launch_pdl(paged_merge_kernel<kD, kNT>, dim3((unsigned)a.units), dim3(32 * kMergeWarps), 0, st, a);
@@ -760,7 +792,7 @@ bool paged_decode_supported(const PagedShape &s) {
 
 size_t paged_decode_scratch(const PagedShape &s) {
     const size_t units = (size_t)s.B * s.Hsel * head_groups(s);
-    return ((units * sizeof(int2) + 255) & ~(size_t)255) + (size_t)kMaxGrid * kWarps * 2 * rec_bytes(s);
+    return ((units * sizeof(int2) + 255) & ~(size_t)255) + (size_t)kMaxGrid * kMaxWarps * 2 * rec_bytes(s);
 }
 
 cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
