@@ -64,7 +64,6 @@ struct DecArgs {
     float *rec;          // [ranges][2] records
     int units, hg;       // units = B * Hsel * hg; hg head groups per list
     int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
-    int tiles;           // 16-key tiles per stage
 };
 
 // A part's record for the stage that reads it.
@@ -251,7 +250,11 @@ struct Batch {
     float gate;
 };
 
-template <int kD, int kCode, int kNT>
+// kSingle: a stage is one part, so one page.  Every stage is worked through as
+// 64 keys without a branch (a missing tile's keys are masked like a missing
+// key): branches around the tiles had cut the arithmetic into pieces too short
+// to hide its latencies, 1.6 times the time.
+template <int kD, int kCode, int kNT, bool kSingle>
 __global__ void __launch_bounds__(32 * warps_of<kNT>(), 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DecArgs a) {
     constexpr uint32_t kHalfBytes = 64 * kD;
@@ -417,7 +420,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
     const uint32_t part_bytes = (uint32_t)a.rows * kD;
     // tile t of a stage lies in part t >> psh, as its (t & pmask)th 16 keys
-    const int psh = a.pps == 1 ? 2 : (a.rows >> 4) - 1, pmask = (1 << psh) - 1;
+    const int psh = kSingle ? 2 : (a.rows >> 4) - 1, pmask = (1 << psh) - 1;
     // The next stage: its keys go out once the stage at hand has made its
     // scores, its values once that one has used its own, so one stage of
     // memory keeps one load in flight behind the arithmetic.
@@ -435,13 +438,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             open(nxt);
         }
         const int first = ci * a.pps, at = first + lane;
-        const int nk = lane < a.pps ? parts[warp][batch & 1][at].nk : a.rows;
+        const int nk = lane < a.pps ? parts[warp][batch & 1][at].nk : 64;
         const unsigned lives = __ballot_sync(~0u, lane < a.pps && nk > 0);
         n_bytes = part_bytes * __popc(lives);
         n_first = 32 * (batch & 1) + first;
         n_unit = cu_unit;
         n_flags = (cu_flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cu_flags & F_NEW : 0) |
-                  (ci == cu_n - 1 ? cu_flags & F_LAST : 0) | (__any_sync(~0u, nk < a.rows) ? F_TAIL : 0);
+                  (ci == cu_n - 1 ? cu_flags & F_LAST : 0) | (__any_sync(~0u, nk < (kSingle ? 64 : a.rows)) ? F_TAIL : 0);
         if (lane == 0) {
             if (n_bytes) mbar_expect_tx(bar_k, n_bytes);
             else mbar_arrive(bar_k);
@@ -527,12 +530,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             uint32_t kr[4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                if (t < a.tiles) ldsm4(kb + swz<kD>(16 * t + mrow, 2 * k + mch), kr[t]);
+                ldsm4(kb + swz<kD>(16 * t + mrow, 2 * k + mch), kr[t]);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    if (t >= a.tiles) continue;
                     const uint32_t *r = kr[t] + 2 * half;
                     uint32_t p0, q0, p1, q1;
                     to_h2<kCode, false>(r[0], p0, q0);
@@ -551,7 +553,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const Part pt = part[t >> psh];
-            const int nk = t < a.tiles ? pt.nk - 16 * (t & pmask) : 0;
+            const int nk = pt.nk - 16 * (t & pmask);
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -644,7 +646,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         // O^T += V^T P^T, 32 dimensions at a time
         ok = mbar_wait_lazy(bar_v, done & 1, &abort_s, a.status);
         if (!__all_sync(~0u, ok)) break;
-        const bool one_page = a.pps == 1;
         const float vs0 = part[0].vs;
         const bool blank = kCode == SA_E4M3 && (flags & F_TAIL);   // what is not a key may hold NaN codes
 #pragma unroll
@@ -652,7 +653,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             uint32_t vr[4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                if (t < a.tiles) ldsm4t(vb + swz<kD>(16 * t + mrow, 2 * np + mch), vr[t]);
+                ldsm4t(vb + swz<kD>(16 * t + mrow, 2 * np + mch), vr[t]);
             float d[2][kNT][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -660,7 +661,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 for (int n = 0; n < kNT; ++n) d[h][n][0] = d[h][n][1] = d[h][n][2] = d[h][n][3] = 0.f;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                if (t >= a.tiles) continue;
                 uint32_t *r = vr[t];
                 if (blank) {
                     const int nk = part[t >> psh].nk - 16 * (t & pmask);
@@ -679,7 +679,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int n = 0; n < kNT; ++n) mma_f16(d[h][n], a0, a1, a2, a3, pb[t][n][0], pb[t][n][1]);
                 }
-                if (!one_page) {
+                if constexpr (!kSingle) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -691,7 +691,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                             }
                 }
             }
-            if (one_page) {
+            if constexpr (kSingle) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -772,7 +772,7 @@ constexpr int kMaxGrid = 148;
 template <int kD, int kCode, int kNT>
 cudaError_t run(const DecArgs &a, int grid, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
     constexpr int smem = warps_of<kNT>() * 2 * 64 * kD + 1024;
-    auto kern = paged_decode_kernel<kD, kCode, kNT>;
+    auto kern = a.pps == 1 ? paged_decode_kernel<kD, kCode, kNT, true> : paged_decode_kernel<kD, kCode, kNT, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(32 * warps_of<kNT>()), smem, st, mk, mv, a);
@@ -814,7 +814,6 @@ cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedC
     a.sub = s.bs > 64 ? 2 : 1;
     a.rows = s.bs > 64 ? (s.bs + 31) / 32 * 16 : s.bs;
     a.pps = (s.flags & SA_HIER) ? 1 : 64 / a.rows;
-    a.tiles = a.rows * a.pps / 16;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     CUtensorMap mk, mv;
