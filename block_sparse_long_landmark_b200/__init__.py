@@ -631,132 +631,160 @@ def paged_cache(p: sa_paged_params, device="cuda"):
             torch.zeros(shape[:2], dtype=torch.float32, device=device))
 
 
+_PAGED_TYPES = None      # (e4m3, int8, bf16, fp32, int32, int64) once torch is there
+
+
+def _paged_types():
+    global _PAGED_TYPES
+    if _PAGED_TYPES is None:
+        t = _torch()
+        _PAGED_TYPES = (t.float8_e4m3fn, t.int8, t.bfloat16, t.float32, t.int32, t.int64)
+    return _PAGED_TYPES
+
+
+def _refuse(what, name, t, dtype, numel, device):
+    raise SparseAttnError(SA_ERR_ARG, f"{what}: {name} must be a dense {dtype} tensor of {numel} elements on device "
+                                      f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def _same(what, device, *checks):
     """Refuses a tensor of another type, size or device, or one that is not dense."""
     for name, t, dtype, numel in checks:
-        if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
-            raise SparseAttnError(SA_ERR_ARG, f"{what}: {name} must be a dense {dtype} tensor of {numel} elements on "
-                                              f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.dtype is not dtype or t.numel() != numel or t.get_device() != device or not t.is_contiguous():
+            _refuse(what, name, t, dtype, numel, device)
 
 
-def _cache_checks(p, cache):
-    torch = _torch()
+def _paged_cache(what, p, cache):
+    """The cache's device, after the same checks."""
+    e4m3, i8, _, f32, _, _ = _paged_types()
     K8, V8, ks, vs = cache
-    ct = torch.float8_e4m3fn if p.code == SA_E4M3 else torch.int8
+    ct = i8 if p.code else e4m3
     n = p.pages * p.Hkv
-    return (("K codes", K8, ct, n * p.block * p.d), ("V codes", V8, ct, n * p.block * p.d),
-            ("K scales", ks, torch.float32, n), ("V scales", vs, torch.float32, n))
+    dev, m = K8.get_device(), n * p.block * p.d
+    _same(what, dev, ("K codes", K8, ct, m), ("V codes", V8, ct, m), ("K scales", ks, f32, n), ("V scales", vs, f32, n))
+    return dev
 
 
-def _on(device, stream, fn, *args):
-    """Runs fn(*args, stream) with `device` current."""
+def _paged_call(what, device, stream, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream unless
+    one is given; raises on an error code."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+    if device < 0:
+        raise SparseAttnError(SA_ERR_ARG, f"{what}: tensors must be on a CUDA device")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _paged_call(what, device, stream, fn, *args)
+    st = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    rc = fn(*args, st)
+    if rc != SA_OK:
+        raise SparseAttnError(rc, what)
 
 
-def _row_strides(what, p, K, V):
+def _row_strides(what, p, K, V, device):
     """(token, head) strides of packed rows [tokens, Hkv, d] whose last
     dimension is dense; K and V alike."""
-    dt = _tdtype(p)
-    for t in (K, V):
-        if t.dtype != dt or tuple(t.shape) != (p.tokens, p.Hkv, p.d) or t.device != K.device or \
-                (t.numel() and (t.stride() != K.stride() or t.stride(2) != 1)):
-            raise SparseAttnError(SA_ERR_ARG, f"{what}: K and V must be {dt} [{p.tokens}, {p.Hkv}, {p.d}] with the same "
-                                              "strides and a dense last dimension")
-    hs = K.stride(1) if p.Hkv > 1 else p.d
-    return (K.stride(0) if p.tokens > 1 else p.Hkv * hs), hs
+    types = _paged_types()
+    dt, shape, st = types[3] if p.dtype else types[2], (p.tokens, p.Hkv, p.d), K.stride()
+    for name, t in (("K", K), ("V", V)):
+        if t.dtype is not dt or t.shape != shape or t.get_device() != device or \
+                (t.numel() and (t.stride() != st or st[2] != 1)):
+            raise SparseAttnError(SA_ERR_ARG, f"{what}: {name} must be {dt} {shape} on device {device} with the strides "
+                                              "of the other and a dense last dimension")
+    hs = st[1] if shape[1] > 1 else shape[2]
+    return (st[0] if shape[0] > 1 else shape[1] * hs), hs
 
 
 def paged_tables(p: sa_paged_params, cur_len, new_len, free_pages, n_free, table, ws, out=None, stream=None):
     """Block table (in place) and slot map of a step: (n_free, cu, slot)."""
-    torch = _torch()
-    dev, i32 = table.device, torch.int32
+    _, _, _, _, i32, i64 = _paged_types()
+    B, tokens = p.B, p.tokens
     if out is None:
-        out = (torch.empty(1, dtype=i32, device=dev), torch.empty(p.B + 1, dtype=i32, device=dev),
-               torch.empty(p.tokens, dtype=torch.int64, device=dev))
+        out = (n_free.new_empty(1), cur_len.new_empty(B + 1), table.new_empty(tokens, dtype=i64))
     n_out, cu, slot = out
-    _same("paged_tables", dev, ("cur_len", cur_len, i32, p.B), ("new_len", new_len, i32, p.B),
-          ("free_pages", free_pages, i32, p.pages), ("n_free", n_free, i32, 1), ("table", table, i32, p.B * p.max_blocks),
-          ("n_free_out", n_out, i32, 1), ("cu", cu, i32, p.B + 1), ("slot", slot, torch.int64, p.tokens))
-    _check(_on(dev, stream, sparse_attn_paged_tables, p, _ptr(cur_len), _ptr(new_len), _ptr(free_pages), _ptr(n_free),
-               _ptr(n_out), _ptr(table), _ptr(cu), _ptr(slot), _ptr(ws), ws.numel()), "sparse_attn_paged_tables")
+    dev = table.get_device()
+    _same("paged_tables", dev, ("cur_len", cur_len, i32, B), ("new_len", new_len, i32, B),
+          ("free_pages", free_pages, i32, p.pages), ("n_free", n_free, i32, 1), ("table", table, i32, B * p.max_blocks),
+          ("n_free_out", n_out, i32, 1), ("cu", cu, i32, B + 1), ("slot", slot, i64, tokens))
+    _paged_call("sparse_attn_paged_tables", dev, stream, lib().sparse_attn_paged_tables, p, cur_len.data_ptr(),
+                new_len.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), n_out.data_ptr(), table.data_ptr(),
+                cu.data_ptr(), slot.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
 def paged_append(p: sa_paged_params, K, V, slot, cache, ws, cu=None, new_len=None, L=None, stream=None):
     """Quantises K, V [tokens, Hkv, d] (strided rows allowed) into the cache at
     `slot`; with L, cu and new_len also the landmarks of the touched blocks."""
-    torch = _torch()
-    dev = cache[0].device
-    ts, hs = _row_strides("paged_append", p, K, V)
-    checks = _cache_checks(p, cache) + (("slot", slot, torch.int64, p.tokens),)
+    types = _paged_types()
+    dev = _paged_cache("paged_append", p, cache)
+    ts, hs = _row_strides("paged_append", p, K, V, dev)
+    _same("paged_append", dev, ("slot", slot, types[5], p.tokens))
     if L is not None:
         if cu is None or new_len is None:
             raise SparseAttnError(SA_ERR_ARG, "paged_append: landmarks need cu and new_len")
-        checks += (("L", L, _tdtype(p), p.B * p.Hkv * p.max_blocks * p.d), ("cu", cu, torch.int32, p.B + 1),
-                   ("new_len", new_len, torch.int32, p.B))
-    if K.device != dev:
-        raise SparseAttnError(SA_ERR_ARG, f"paged_append: K and V must be on {dev}")
-    _same("paged_append", dev, *checks)
-    _check(_on(dev, stream, sparse_attn_paged_append, p, _ptr(K), _ptr(V), ts, hs, _ptr(slot), _ptr(cu),
-               _ptr(new_len), *map(_ptr, cache), _ptr(L), _ptr(ws), ws.numel()), "sparse_attn_paged_append")
+        _same("paged_append", dev, ("L", L, types[3] if p.dtype else types[2], p.B * p.Hkv * p.max_blocks * p.d),
+              ("cu", cu, types[4], p.B + 1), ("new_len", new_len, types[4], p.B))
+    K8, V8, ks, vs = cache
+    _paged_call("sparse_attn_paged_append", dev, stream, lib().sparse_attn_paged_append, p, K.data_ptr(), V.data_ptr(),
+                ts, hs, slot.data_ptr(), _ptr(cu), _ptr(new_len), K8.data_ptr(), V8.data_ptr(), ks.data_ptr(),
+                vs.data_ptr(), _ptr(L), ws.data_ptr(), ws.numel())
     return cache
 
 
 def paged_gather(p: sa_paged_params, slot, cache, ws, out=None, stream=None):
     """The cached keys and values at `slot`: (K, V) [tokens, Hkv, d]."""
-    torch = _torch()
-    dev = cache[0].device
+    types = _paged_types()
+    dev = _paged_cache("paged_gather", p, cache)
+    K8, V8, ks, vs = cache
     if out is None:
-        out = tuple(torch.empty(p.tokens, p.Hkv, p.d, dtype=_tdtype(p), device=dev) for _ in "kv")
-    ts, hs = _row_strides("paged_gather", p, *out)
-    _same("paged_gather", dev, *_cache_checks(p, cache), ("slot", slot, torch.int64, p.tokens))
-    if out[0].device != dev:
-        raise SparseAttnError(SA_ERR_ARG, f"paged_gather: K and V must be on {dev}")
-    _check(_on(dev, stream, sparse_attn_paged_gather, p, _ptr(slot), *map(_ptr, cache), _ptr(out[0]), _ptr(out[1]),
-               ts, hs, _ptr(ws), ws.numel()), "sparse_attn_paged_gather")
+        dt, shape = types[3] if p.dtype else types[2], (p.tokens, p.Hkv, p.d)
+        out = (ks.new_empty(shape, dtype=dt), ks.new_empty(shape, dtype=dt))
+    K, V = out
+    ts, hs = _row_strides("paged_gather", p, K, V, dev)
+    _same("paged_gather", dev, ("slot", slot, types[5], p.tokens))
+    _paged_call("sparse_attn_paged_gather", dev, stream, lib().sparse_attn_paged_gather, p, slot.data_ptr(),
+                K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), K.data_ptr(), V.data_ptr(), ts, hs,
+                ws.data_ptr(), ws.numel())
     return out
 
 
 def paged_decode(p: sa_paged_params, q, cache, table, seq_len, ws, lists=None, out=None, stream=None):
     """One query per sequence over the cache: (o, lse).  lists = (idx, score,
     count) of select_decode_varlen, or None for every block."""
-    torch = _torch()
-    dev, i32 = cache[0].device, torch.int32
-    if out is None:
-        out = (torch.empty_like(q), torch.empty(p.B, p.Hq, dtype=torch.float32, device=dev))
-    o, lse = out
-    n, dt = p.B * p.Hq, _tdtype(p)
-    checks = _cache_checks(p, cache) + (("q", q, dt, n * p.d), ("o", o, dt, n * p.d), ("lse", lse, torch.float32, n),
-                                        ("table", table, i32, p.B * p.max_blocks), ("seq_len", seq_len, i32, p.B))
-    idx, sc, cnt = lists if lists is not None else (None, None, None)
+    types = _paged_types()
+    f32, i32, dt = types[3], types[4], types[3] if p.dtype else types[2]
+    dev = _paged_cache("paged_decode", p, cache)
+    K8, V8, ks, vs = cache
+    B = p.B
+    n = B * p.Hq
+    o, lse = out if out is not None else (q.new_empty(q.shape), ks.new_empty((B, p.Hq)))
+    _same("paged_decode", dev, ("q", q, dt, n * p.d), ("o", o, dt, n * p.d), ("lse", lse, f32, n),
+          ("table", table, i32, B * p.max_blocks), ("seq_len", seq_len, i32, B))
+    idx = sc = cnt = None
     if lists is not None:
-        u = p.B * _hsel(p)
-        checks += (("idx", idx, i32, u * (p.top_k + 2)), ("score", sc, torch.float32, u * (p.top_k + 2)),
-                   ("count", cnt, i32, u))
-    _same("paged_decode", dev, *checks)
-    _check(_on(dev, stream, sparse_attn_paged_decode, p, _ptr(q), *map(_ptr, cache), _ptr(table), _ptr(seq_len),
-               _ptr(idx), _ptr(sc), _ptr(cnt), _ptr(o), _ptr(lse), _ptr(ws), ws.numel()), "sparse_attn_paged_decode")
-    return out
+        idx, sc, cnt = lists
+        u = B * _hsel(p)
+        m = u * (p.top_k + 2)
+        _same("paged_decode", dev, ("idx", idx, i32, m), ("score", sc, f32, m), ("count", cnt, i32, u))
+    _paged_call("sparse_attn_paged_decode", dev, stream, lib().sparse_attn_paged_decode, p, q.data_ptr(),
+                K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(), seq_len.data_ptr(),
+                _ptr(idx), _ptr(sc), _ptr(cnt), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return o, lse
 
 
 def paged_prefill(p: sa_paged_params, Q, cu, cache, table, seq_len, ws, out=None, stream=None):
     """Packed query chunks [tokens, Hq, d] over the cache: (O, lse [tokens, Hq])."""
-    torch = _torch()
-    dev, i32 = cache[0].device, torch.int32
-    if out is None:
-        out = (torch.empty_like(Q), torch.empty(p.tokens, p.Hq, dtype=torch.float32, device=dev))
-    O, lse = out
-    n, dt = p.tokens * p.Hq, _tdtype(p)
-    _same("paged_prefill", dev, *_cache_checks(p, cache), ("Q", Q, dt, n * p.d), ("O", O, dt, n * p.d),
-          ("lse", lse, torch.float32, n), ("cu", cu, i32, p.B + 1), ("table", table, i32, p.B * p.max_blocks),
-          ("seq_len", seq_len, i32, p.B))
-    _check(_on(dev, stream, sparse_attn_paged_prefill, p, _ptr(Q), _ptr(cu), *map(_ptr, cache), _ptr(table),
-               _ptr(seq_len), _ptr(O), _ptr(lse), _ptr(ws), ws.numel()), "sparse_attn_paged_prefill")
-    return out
+    types = _paged_types()
+    f32, i32, dt = types[3], types[4], types[3] if p.dtype else types[2]
+    dev = _paged_cache("paged_prefill", p, cache)
+    K8, V8, ks, vs = cache
+    n = p.tokens * p.Hq
+    O, lse = out if out is not None else (Q.new_empty(Q.shape), ks.new_empty((p.tokens, p.Hq)))
+    _same("paged_prefill", dev, ("Q", Q, dt, n * p.d), ("O", O, dt, n * p.d), ("lse", lse, f32, n),
+          ("cu", cu, i32, p.B + 1), ("table", table, i32, p.B * p.max_blocks), ("seq_len", seq_len, i32, p.B))
+    _paged_call("sparse_attn_paged_prefill", dev, stream, lib().sparse_attn_paged_prefill, p, Q.data_ptr(),
+                cu.data_ptr(), K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(),
+                seq_len.data_ptr(), O.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return O, lse
 
 
 def lsa_tree_levels(p: sa_lsa_params, fanout: int, tree):

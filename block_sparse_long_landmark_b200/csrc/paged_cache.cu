@@ -149,13 +149,6 @@ paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t
 // Append
 // ---------------------------------------------------------------------------
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) { load16(p, f); }
-__device__ __forceinline__ void load8(const float *p, float *f) {
-    load16(p, f);
-    load16(p + 4, f + 4);
-}
-
 // The smallest power of two s >= 2^-126 with amax <= M s (M = 448 or 127), from
 // the bits of the finite amax: amax = 1.f * 2^x fits M 2^e exactly when
 // 1.f <= 1.75 (e4m3; 1.984375 for int8) at e = x - 8 (x - 6), else one more.
@@ -169,161 +162,327 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float((unsigned)(e + 127) << 23);
 }
 
-constexpr int kAppThreads = 256;   // 128 for the keys, 128 for the values
+constexpr int kAppThreads = 128;
 constexpr int kWinMax = 64;        // tokens whose runs one CTA looks for
 
-// A run: consecutive slots of one page.  The CTA of (window, head) takes the
-// runs that begin in its window: it finds the new rows' largest magnitude,
-// keeps the block's scale when they fit, else takes the power of two that
-// holds them and rounds the codes already there anew (scales are powers of
-// two, so a scaled value is exact and a code is one rounding of it), writes
-// the codes, and means the block's cached keys into its landmark.
-template <typename T, int kCode, int kD>
-__global__ void __launch_bounds__(kAppThreads)
+// Eight elements as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+    // eight codes in the same registers
+    __device__ __forceinline__ void hold(uint2 c) { a.x = c.x, a.y = c.y; }
+    __device__ __forceinline__ uint2 held() const { return make_uint2(a.x, a.y); }
+    // bits of the largest magnitude, as fp32 (a NaN's are above infinity's)
+    __device__ __forceinline__ unsigned top() const {
+        const unsigned m = 0x7fff7fffu;
+        const unsigned x = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+        return max(x << 16, x & 0xffff0000u);
+    }
+    __device__ __forceinline__ void get(float *f) const {
+        const unsigned w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void hold(uint2 c) { a.x = __uint_as_float(c.x), a.y = __uint_as_float(c.y); }
+    __device__ __forceinline__ uint2 held() const { return make_uint2(__float_as_uint(a.x), __float_as_uint(a.y)); }
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ unsigned top() const {
+        float f[8];
+        get(f);
+        unsigned x = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x = max(x, __float_as_uint(f[i]) & 0x7fffffffu);
+        return x;
+    }
+    __device__ __forceinline__ void get(float *f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+
+// Sum of eight columns' codes: as fp32 (e4m3) or as whole numbers (int8).
+template <int kCode> struct Sum8;
+template <> struct Sum8<SA_E4M3> {
+    float v[8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    __device__ __forceinline__ void add(uint2 c) {
+        float f[8];
+        code_values4<SA_E4M3>(c.x, f);
+        code_values4<SA_E4M3>(c.y, f + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += f[e];
+    }
+    __device__ __forceinline__ float get(int e) const { return v[e]; }
+};
+template <> struct Sum8<SA_INT8> {
+    int v[8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0;
+    }
+    __device__ __forceinline__ void add(uint2 c) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += (int)((e < 4 ? c.x : c.y) << (24 - 8 * (e & 3))) >> 24;
+    }
+    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+};
+
+// Eight finite values with |y inv| <= M to codes, inv a power of two.
+template <int kCode>
+__device__ __forceinline__ uint2 encode8(const float *y, float inv) {
+    uint2 c;
+    if (kCode == SA_E4M3) {
+        c.x = codes_of2<kCode>(y[0] * inv, y[1] * inv) | codes_of2<kCode>(y[2] * inv, y[3] * inv) << 16;
+        c.y = codes_of2<kCode>(y[4] * inv, y[5] * inv) | codes_of2<kCode>(y[6] * inv, y[7] * inv) << 16;
+    } else {
+        // adding 1.5 * 2^23 rounds to a whole number whose low byte is the code
+        unsigned b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(y[i], inv, 12582912.f));
+        c.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        c.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    }
+    return c;
+}
+// The same for any values and any scale: NaN becomes 0, what is beyond M (an
+// infinity) the largest code.
+template <int kCode>
+__device__ uint2 encode8_any(const float *y, float scale) {
+    constexpr float kMost = kCode == SA_E4M3 ? 448.f : 127.f;
+    float v[8];
+    for (int i = 0; i < 8; ++i) {
+        const float q = __fdiv_rn(y[i], scale);
+        v[i] = isnan(q) ? 0.f : fminf(fmaxf(q, -kMost), kMost);
+    }
+    return encode8<kCode>(v, 1.f);
+}
+
+// Last index b in [0, n) with off[b] <= x, found by a whole warp, 32 probes a
+// round (off ascending, off[0] <= x).
+__device__ __forceinline__ int warp_owner(const int *off, int n, int x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+        const unsigned le = __ballot_sync(~0u, i < hi && off[i] <= x) | 1u;
+        lo += (31 - __clz((int)le)) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// A run: consecutive slots of one page.  The CTA of (window, head, keys or
+// values) takes the runs that begin in its window.  A run's new rows, and for the landmark the codes
+// already in the block, are read into registers once: their largest magnitude
+// decides the scale (kept when the rows fit, else the power of two that holds
+// them, and the codes already there are rounded anew; scales are powers of
+// two, so a scaled value is exact and a code is one rounding of it), then the
+// codes are written and the block's cached keys meant into its landmark.
+// HBM bound for prompts (two bytes in, one out per value); a step of single
+// tokens is bound by its chain of reads: slot, rows, scale.
+template <typename T, int kCode, int kD, int kRows>
+__global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? (kRows == 64 ? 8 : 5) : kRows == 64 ? 4 : 2)
 paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__ V, long long ts, long long hs,
                     const int64_t *__restrict__ slot, const int32_t *__restrict__ cu,
                     const int32_t *__restrict__ new_len, uint8_t *K8, uint8_t *V8, float *ks, float *vs, T *L,
                     int window, unsigned *status) {
     constexpr int VPR = kD / 8;           // vectors of eight per row
     constexpr int RS = 128 / VPR;         // rows per step of a half
+    constexpr int NV = kRows / RS;        // steps per block
     constexpr float kMost = kCode == SA_E4M3 ? 448.f : 127.f;
-    __shared__ int sl[kWinMax + 129];     // slots from the token before the window on
-    __shared__ unsigned brk[(kWinMax + 129 + 31) / 32 + 1];
-    __shared__ float red[2][4];
+    constexpr int kSpan = kWinMax + 128;  // tokens looked at: the window and the end of its last run
+    __shared__ int sl[kSpan + 1];         // slots from the token before the window on
+    __shared__ unsigned brk[kSpan / 32 + 1], lead[kWinMax / 32];
+    __shared__ unsigned red[4];
     __shared__ float lsum[4][kD];
-    const int tid = threadIdx.x, lane = tid & 31, half = tid >> 7, t = tid & 127, w4 = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, w4 = t >> 5;
     const int cv = t % VPR, rs = t / VPR;
-    const int h = blockIdx.y, bs = s.bs;
-    const long long w0 = (long long)blockIdx.x * window;
+    // keys and values of every head of a window are neighbours in the grid:
+    // they read the same rows of their tensors
+    const bool half = blockIdx.x & 1;
+    const int h = (blockIdx.x >> 1) % s.Hkv, bs = s.bs;
+    const long long w0 = (long long)((blockIdx.x >> 1) / s.Hkv) * window;
     const int span = (int)min((long long)window + bs, (long long)s.tokens - w0);   // tokens w0 .. w0 + span - 1
     // sl[j + 1] = slot of token w0 + j, -1 when there is none or it is out of range
-    if (tid <= span && tid < kWinMax + 129) {
-        const long long i = w0 + tid - 1;
+    for (int j = t; j <= span; j += kAppThreads) {
+        const long long i = w0 + j - 1;
         const long long x = i >= 0 ? slot[i] : -1;
         const bool good = x >= 0 && x < (long long)s.pages * bs;
         if (x >= 0 && !good) set_status(status, kStatusBadIndex);
-        sl[tid] = good ? (int)x : -1;
+        sl[j] = good ? (int)x : -1;
     }
     __syncthreads();
-    {
+    for (int j = t; j < kSpan + 32; j += kAppThreads) {
         // bit j of brk: a run ends before token w0 + j
-        const int j = tid;
         const bool b = j >= span || sl[j + 1] < 0 || sl[j + 1] != sl[j] + 1 || sl[j] < 0 || sl[j + 1] % bs == 0;
         const unsigned m = __ballot_sync(~0u, b);
-        if (lane == 0 && (tid >> 5) < (int)(sizeof(brk) / 4)) brk[tid >> 5] = m;
+        const unsigned f = __ballot_sync(~0u, b && j < min(window, span) && sl[j + 1] >= 0);   // a run begins here
+        if (lane == 0) {
+            brk[j >> 5] = m;
+            if (j < kWinMax) lead[j >> 5] = f;
+        }
     }
     __syncthreads();
     const T *src = half ? V : K;
     uint8_t *codes = half ? V8 : K8;
     float *scales = half ? vs : ks;
-    for (int j = 0; j < min(window, span); ++j) {
-        const int first = sl[j + 1];
-        if (first < 0 || !((brk[j >> 5] >> (j & 31)) & 1u)) continue;
+    const bool mean = !half && L;
+    for (int w = 0; w < kWinMax / 32; ++w)
+    for (unsigned left = lead[w]; left; left &= left - 1) {
+        const int j = 32 * w + __ffs(left) - 1, first = sl[j + 1];
         int end = j + 1;                  // next break (a set bit always follows: bits from span on are set)
         while (!((brk[end >> 5] >> (end & 31)) & 1u)) {
             const unsigned rest = brk[end >> 5] >> (end & 31);
             end = rest ? end + __ffs(rest) - 1 : (end | 31) + 1;
         }
         const int n = end - j, page = first / bs, off = first - page * bs;
-        const T *x0 = src + (w0 + j) * ts + (long long)h * hs + cv * 8;
+        const T *x0 = src + (w0 + j - off) * ts + (long long)h * hs + cv * 8;   // row r of the block: x0 + r ts
         uint8_t *blk = codes + ((size_t)page * s.Hkv + h) * bs * kD + cv * 8;
         float *scale_at = scales + (size_t)page * s.Hkv + h;
         const float was = off > 0 ? *scale_at : 0.f;
-        // largest finite magnitude of the new rows
-        float am = 0.f;
-        bool odd = false;
-        for (int r = rs; r < n; r += RS) {
-            float f[8];
-            load8(x0 + r * ts, f);
+        // block rows rs, rs + RS, ...: codes already there, or new rows
+        Raw8<T> x[NV];
+        unsigned top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float m = fabsf(f[i]);
-                const bool fin = m <= 3.402823466e38f;
-                odd |= !fin;
-                am = fin ? fmaxf(am, m) : am;
+        for (int k = 0; k < NV; ++k) {
+            const int r = rs + RS * k;
+            if (r >= off && r < off + n) x[k].load(x0 + r * ts);
+            else if (mean && r < off) x[k].hold(*reinterpret_cast<const uint2 *>(blk + (size_t)r * kD));
+        }
+        // the landmark's place
+        int b = 0, pos = -1;
+        if (mean) {
+            const int i = (int)(w0 + j), last = cu[s.B];
+            b = warp_owner(cu, s.B, min(i, last - 1));
+            if (i < last) pos = new_len[b] - cu[b + 1] + i;
+            if (pos < 0 || pos % bs != off || pos / bs >= s.maxb) {
+                if (t == 0) set_status(status, kStatusBadIndex);
+                pos = -1;
             }
         }
-        if (odd) set_status(status, kStatusNaN);
-        am = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(am)));
-        if (lane == 0) red[half][w4] = am;
-        asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
-        am = fmaxf(fmaxf(red[half][0], red[half][1]), fmaxf(red[half][2], red[half][3]));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int r = rs + RS * k;
+            if (r >= off && r < off + n) top = max(top, x[k].top());
+        }
+        top = __reduce_max_sync(~0u, top);
+        if (lane == 0) red[w4] = top;
+        __syncthreads();
+        top = max(max(red[0], red[1]), max(red[2], red[3]));
+        const bool odd = top >= 0x7f800000u;
+        if (odd) {
+            // not all finite: the largest of those that are
+            if (t == 0) set_status(status, kStatusNaN);
+            top = 0;
+#pragma unroll 1
+            for (int r = rs; r < off + n; r += RS) {
+                if (r < off) continue;
+                Raw8<T> z;
+                z.load(x0 + r * ts);
+                float f[8];
+                z.get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const unsigned u = __float_as_uint(f[e]) & 0x7fffffffu;
+                    top = max(top, u < 0x7f800000u ? u : 0u);
+                }
+            }
+            top = __reduce_max_sync(~0u, top);
+            __syncthreads();   // red was read by all
+            if (lane == 0) red[w4] = top;
+            __syncthreads();
+            top = max(max(red[0], red[1]), max(red[2], red[3]));
+        }
+        const float am = __uint_as_float(top);
         const bool usable = was >= 1.17549435e-38f && was <= 3.402823466e38f;
         const bool fits = off > 0 && usable && am <= kMost * was;
         const float now = fits ? was : scale_for<kCode>(am);
-        // a power of two divides exactly by its reciprocal; a kept scale may be any number
-        const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
-        const float inv = __fdiv_rn(1.f, now);
-        const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
-        float acc[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-        // codes already in the block
-        if (!fits || (half == 0 && L)) {
+        Sum8<kCode> sum;
+        sum.zero();
+        // codes already there: as they are, or rounded anew to the grown scale
+        if (!fits) {
+            const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
+#pragma unroll 1
             for (int r = rs; r < off; r += RS) {
-                uint2 c = *reinterpret_cast<const uint2 *>(blk + (size_t)r * kD);
-                float f[8];
-                code_values4<kCode>(c.x, f);
-                code_values4<kCode>(c.y, f + 4);
-                if (!fits) {
+                uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD), c = *at;
+                float y[8];
+                code_values4<kCode>(c.x, y);
+                code_values4<kCode>(c.y, y + 4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= ratio;
-                    c.x = codes_of2<kCode>(f[0], f[1]) | codes_of2<kCode>(f[2], f[3]) << 16;
-                    c.y = codes_of2<kCode>(f[4], f[5]) | codes_of2<kCode>(f[6], f[7]) << 16;
-                    *reinterpret_cast<uint2 *>(blk + (size_t)r * kD) = c;
-                    code_values4<kCode>(c.x, f);
-                    code_values4<kCode>(c.y, f + 4);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+                for (int e = 0; e < 8; ++e) y[e] *= ratio;
+                c = encode8<kCode>(y, 1.f);
+                *at = c;
+                if (mean) sum.add(c);
             }
+        } else if (mean) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (rs + RS * k < off) sum.add(x[k].held());
         }
-        // the new rows: NaN becomes 0, infinities the largest code
-        for (int r = rs; r < n; r += RS) {
-            float f[8];
-            load8(x0 + r * ts, f);
+        // the new rows: a power of two divides exactly by its reciprocal; a
+        // kept scale may be any number
+        if (!odd && (__float_as_uint(now) & 0x7fffffu) == 0) {
+            const float inv = __fdiv_rn(1.f, now);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = pow2 ? f[i] * inv : __fdiv_rn(f[i], now);
-                f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(y, -kMost), kMost);
+            for (int k = 0; k < NV; ++k) {
+                const int r = rs + RS * k;
+                if (r < off || r >= off + n) continue;
+                float y[8];
+                x[k].get(y);
+                const uint2 c = encode8<kCode>(y, inv);
+                *reinterpret_cast<uint2 *>(blk + (size_t)r * kD) = c;
+                if (mean) sum.add(c);
             }
-            uint2 c;
-            c.x = codes_of2<kCode>(f[0], f[1]) | codes_of2<kCode>(f[2], f[3]) << 16;
-            c.y = codes_of2<kCode>(f[4], f[5]) | codes_of2<kCode>(f[6], f[7]) << 16;
-            *reinterpret_cast<uint2 *>(blk + (size_t)(off + r) * kD) = c;
-            if (half == 0 && L) {
-                code_values4<kCode>(c.x, f);
-                code_values4<kCode>(c.y, f + 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+        } else {
+#pragma unroll 1
+            for (int r = rs; r < off + n; r += RS) {
+                if (r < off) continue;
+                Raw8<T> z;
+                z.load(x0 + r * ts);
+                float y[8];
+                z.get(y);
+                const uint2 c = encode8_any<kCode>(y, now);
+                *reinterpret_cast<uint2 *>(blk + (size_t)r * kD) = c;
+                if (mean) sum.add(c);
             }
         }
         if (t == 0) *scale_at = now;
-        if (half == 0 && L) {
-            // sums of codes are exact in fp32 up to 2^24 steps of 2^-9 (one
-            // rounding at most in a full block of 128 extreme codes)
-            const long long i = w0 + j;
-            const int b = owner(cu, s.B, (int)min(i, (long long)cu[s.B] - 1));
-            const int pos = new_len[b] - cu[b + 1] + (int)i;
-            const bool good = i < cu[s.B] && pos >= 0 && pos % bs == off && pos / bs < s.maxb;
-            if (!good && t == 0) set_status(status, kStatusBadIndex);
+        if (mean) {
+            // sums of e4m3 codes are exact in fp32 up to 2^24 steps of 2^-9
+            // (one rounding at most in a full block of 128 extreme codes)
+            float acc[8];
 #pragma unroll
-            for (int i2 = 0; i2 < 8; ++i2) {
+            for (int e = 0; e < 8; ++e) acc[e] = sum.get(e);
 #pragma unroll
-                for (int o = VPR; o < 32; o <<= 1) acc[i2] += __shfl_xor_sync(~0u, acc[i2], o);
+            for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                for (int o = VPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(~0u, acc[e], o);
             }
             if (lane < VPR) {
 #pragma unroll
-                for (int i2 = 0; i2 < 8; ++i2) lsum[w4][cv * 8 + i2] = acc[i2];
+                for (int e = 0; e < 8; ++e) lsum[w4][cv * 8 + e] = acc[e];
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (good && t < kD) {
-                const float sum = (lsum[0][t] + lsum[1][t]) + (lsum[2][t] + lsum[3][t]);
-                const float mean = __fdiv_rn(sum * now, (float)(off + n));
-                from_f(L[(((size_t)b * s.Hkv + h) * s.maxb + pos / bs) * kD + t], mean);
+            __syncthreads();
+            if (pos >= 0 && t < kD) {
+                const float all = (lsum[0][t] + lsum[1][t]) + (lsum[2][t] + lsum[3][t]);
+                from_f(L[(((size_t)b * s.Hkv + h) * s.maxb + pos / bs) * kD + t],
+                       __fdiv_rn(all * now, (float)(off + n)));
             }
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+        __syncthreads();
     }
 }
 
@@ -386,8 +545,9 @@ cudaError_t append_t(const PagedShape &s, const void *K, const void *V, long lon
     // cost a CTA each.
     int window = 1;
     while (window < kWinMax && (long long)s.tokens * s.Hkv > (long long)window * 8 * max(1, sm_count())) window <<= 1;
-    const dim3 grid((unsigned)((s.tokens + window - 1) / window), s.Hkv);
-    auto k = s.d == 128 ? paged_append_kernel<T, kCode, 128> : paged_append_kernel<T, kCode, 64>;
+    const unsigned grid = (unsigned)((s.tokens + window - 1) / window * s.Hkv * 2);
+    auto k = s.d == 128 ? (s.bs <= 64 ? paged_append_kernel<T, kCode, 128, 64> : paged_append_kernel<T, kCode, 128, 128>)
+                        : (s.bs <= 64 ? paged_append_kernel<T, kCode, 64, 64> : paged_append_kernel<T, kCode, 64, 128>);
     k<<<grid, kAppThreads, 0, st>>>(s, (const T *)K, (const T *)V, ts, hs, slot, cu, nl, K8, V8, ks, vs, (T *)L,
                                     window, status);
     note_launch();
