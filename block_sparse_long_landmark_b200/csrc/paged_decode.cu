@@ -71,6 +71,9 @@ struct __align__(16) Part {
     float ks, vs, gate;   // key scale, value scale, gate (hierarchical: score), log2 units
     int nk;               // valid keys (0: not loaded)
 };
+struct Place {
+    int y, nk;            // first cache row of a part, its valid keys
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -144,9 +147,11 @@ __device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int u) {
 
 // Entries (blocks) of a unit: its list's, or every block of its sequence.
 __device__ __forceinline__ int entries_of(const DecArgs &a, int u) {
-    const int lu = u / a.hg, n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
+    const int lu = u / a.hg;
+    const int listed = a.l.idx ? a.l.count[lu] : 0;     // both loads in flight
+    const int n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
     if (!a.l.idx) return (n + a.s.bs - 1) / a.s.bs;
-    return n > 0 ? max(0, min(a.l.count[lu], a.s.cap)) : 0;
+    return n > 0 ? max(0, min(listed, a.s.cap)) : 0;
 }
 __device__ __forceinline__ int stages_of(const DecArgs &a, int entries) {
     return (entries * a.sub + a.pps - 1) / a.pps;
@@ -247,7 +252,7 @@ struct Batch {
     int step;                   // load steps done
     int page;                   // lane: block, then page of its part (-1: none)
     int nk;                     // lane: valid keys
-    float gate;
+    float gate, ks, vs;
 };
 
 // kSingle: a stage is one part, so one page.  Every stage is worked through as
@@ -263,7 +268,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dec_raw) + 1023) &
                                                           ~uintptr_t(1023));
     __shared__ Part parts[kWarps][2][32];     // of two batches
-    __shared__ int part_y[kWarps][32];        // first cache row of the batch being issued
+    __shared__ Place places[kWarps][32];      // of the batch being issued
     __shared__ uint64_t bars[kWarps][2];      // the warp's keys, its values
     __shared__ long long pre[kThreads + 1];
     __shared__ long long wtot[kWarps];
@@ -396,18 +401,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 }
             }
         } else {
-            // the records go where the batch before the last one had its own
-            Part p{0.f, 0.f, t.gate, 0};
-            int y = 0;
-            if (t.page >= 0) {
-                const int ph = t.page * s.Hkv + w.g;
-                p.ks = a.c.ks[ph];
-                p.vs = a.c.vs[ph];
-                p.nk = t.nk;
-                y = ph * s.bs + (t.s0 * a.pps + lane) % a.sub * a.rows;
-            }
-            parts[warp][batch & 1][lane] = p;
-            part_y[warp][lane] = y;
+            const int ph = max(t.page, 0) * s.Hkv + w.g;
+            if (t.page < 0) t.nk = 0;
+            places[warp][lane] = Place{ph * s.bs + (t.s0 * a.pps + lane) % a.sub * a.rows, t.nk};
+            // in flight while the first stage's keys are sent for
+            t.ks = t.page >= 0 ? a.c.ks[ph] : 0.f;
+            t.vs = t.page >= 0 ? a.c.vs[ph] : 0.f;
             __syncwarp();
         }
         ++t.step;
@@ -427,7 +426,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     uint32_t n_bytes = 0;
     int n_flags = 0, n_unit = 0, n_first = 0;   // flags, unit and first part (with the batch's half) of that stage
     auto issue_k = [&]() -> bool {              // false: the range is issued
-        if (ci == cu_n) {
+        const bool fresh = ci == cu_n;
+        if (fresh) {
             if (nxt.unit < 0) return false;
             ++batch;
             while (nxt.step < 4) more(nxt);
@@ -435,22 +435,28 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             cu_n = nxt.s1 - nxt.s0;
             cu_flags = nxt.flags;
             ci = 0;
-            open(nxt);
         }
-        const int first = ci * a.pps, at = first + lane;
-        const int nk = lane < a.pps ? parts[warp][batch & 1][at].nk : 64;
-        const unsigned lives = __ballot_sync(~0u, lane < a.pps && nk > 0);
-        n_bytes = part_bytes * __popc(lives);
+        const int first = ci * a.pps;
+        const Place at = places[warp][min(31, first + lane)];
+        const bool live = lane < a.pps && at.nk > 0;
+        n_bytes = part_bytes * __popc(__ballot_sync(~0u, live));
         n_first = 32 * (batch & 1) + first;
         n_unit = cu_unit;
         n_flags = (cu_flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cu_flags & F_NEW : 0) |
-                  (ci == cu_n - 1 ? cu_flags & F_LAST : 0) | (__any_sync(~0u, nk < (kSingle ? 64 : a.rows)) ? F_TAIL : 0);
+                  (ci == cu_n - 1 ? cu_flags & F_LAST : 0) |
+                  (__any_sync(~0u, lane < a.pps && at.nk < (kSingle ? 64 : a.rows)) ? F_TAIL : 0);
         if (lane == 0) {
             if (n_bytes) mbar_expect_tx(bar_k, n_bytes);
             else mbar_arrive(bar_k);
         }
         __syncwarp();
-        if (lane < a.pps && nk > 0) tma_load_2d(kb + lane * part_bytes, &tmK, bar_k, 0, part_y[warp][at]);
+        if (live) tma_load_2d(kb + lane * part_bytes, &tmK, bar_k, 0, at.y);
+        if (fresh) {
+            // the records go where the batch before the last one had its own
+            parts[warp][batch & 1][lane] = Part{nxt.ks, nxt.vs, nxt.gate, nxt.nk};
+            open(nxt);
+            __syncwarp();
+        }
         return true;
     };
     auto issue_v = [&]() {
@@ -459,9 +465,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             else mbar_arrive(bar_v);
         }
         __syncwarp();
-        const int at = ci * a.pps + lane;
-        if (lane < a.pps && parts[warp][batch & 1][at].nk > 0)
-            tma_load_2d(vb + lane * part_bytes, &tmV, bar_v, 0, part_y[warp][at]);
+        const Place at = places[warp][min(31, ci * a.pps + lane)];
+        if (lane < a.pps && at.nk > 0) tma_load_2d(vb + lane * part_bytes, &tmV, bar_v, 0, at.y);
         ++ci;
         if (nxt.unit >= 0 && nxt.step < 3) more(nxt);
     };
@@ -476,8 +481,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     bool ok = true, have = issue_k(), v_out = have, k_next = false;
     if (have) issue_v();
     for (; have; ++done) {
-        ok = mbar_wait_lazy(bar_k, done & 1, &abort_s, a.status);
-        if (!__all_sync(~0u, ok)) break;
         const int flags = n_flags, unit = n_unit;
         const Part *part = &parts[warp][0][n_first];
         if (flags & F_NEW) {
@@ -518,6 +521,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 }
             }
         }
+        ok = mbar_wait_lazy(bar_k, done & 1, &abort_s, a.status);
+        if (!__all_sync(~0u, ok)) break;
         const int mrow = (lane & 7) + (lane & 8), mch = lane >> 4;   // row and chunk of the lane's ldmatrix address
         // S^T = K q^T: 16 keys x 8 heads per tile
         float z[4][kNT][4];
