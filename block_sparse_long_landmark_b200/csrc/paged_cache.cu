@@ -486,6 +486,165 @@ paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__
     }
 }
 
+// The same for few tokens (a step of single tokens): one warp per (token,
+// head, keys or values), the run's first token leading.  Every read of a warp
+// that does not need another is sent off at once -- slots, then scale, new
+// rows, the block's codes and the landmark's place -- and nothing is shared
+// between warps, so the call takes about two round trips to memory.
+template <typename T, int kCode, int kD>
+__global__ void __launch_bounds__(128)
+paged_append_step_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__ V, long long ts, long long hs,
+                         const int64_t *__restrict__ slot, const int32_t *__restrict__ cu,
+                         const int32_t *__restrict__ new_len, uint8_t *K8, uint8_t *V8, float *ks, float *vs, T *L,
+                         unsigned *status) {
+    constexpr int VPR = kD / 8;           // lanes per row, eight columns each
+    constexpr int RS = 32 / VPR;          // rows per step
+    constexpr int NB = 8;                 // steps in flight
+    constexpr float kMost = kCode == SA_E4M3 ? 448.f : 127.f;
+    const int lane = threadIdx.x & 31, cv = lane % VPR, rs = lane / VPR;
+    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const bool val = unit & 1;
+    const int h = (int)((unit >> 1) % s.Hkv), bs = s.bs;
+    const long long i0 = (unit >> 1) / s.Hkv;
+    if (i0 >= s.tokens) return;
+    const long long most = (long long)s.pages * bs;
+    // slots of the tokens before, of and after i0: lane l holds i0 - 1 + l
+    auto slot_at = [&](long long i) { return i >= 0 && i < s.tokens ? slot[i] : -1ll; };
+    const long long mine = slot_at(i0 - 1 + lane);
+    const long long x = __shfl_sync(~0u, mine, 1), before = __shfl_sync(~0u, mine, 0);
+    if (x < 0) return;
+    if (x >= most) {
+        if (lane == 0) set_status(status, kStatusBadIndex);
+        return;
+    }
+    const int first = (int)x, page = first / bs, off = first - page * bs;
+    if (off > 0 && before >= 0 && before + 1 == x) return;      // inside a run
+    // rows of the run: slots go on by one within the page
+    int n = 0;
+    for (int base = 0;; base += 30) {
+        const long long v = base == 0 ? mine : slot_at(i0 - 1 + base + lane);
+        const bool on = lane > 0 && v == x + base + lane - 1 && off + base + lane - 1 < bs;
+        const unsigned stop = ~__ballot_sync(~0u, on) & 0xfffffffeu;
+        n = base + (stop ? __ffs((int)stop) - 2 : 31);
+        if (stop || base + 30 >= bs) break;
+    }
+    n = min(n, bs - off);
+    const T *src = (val ? V : K) + (i0 - off) * ts + (long long)h * hs + cv * 8;      // row r of the block: src + r ts
+    uint8_t *blk = (val ? V8 : K8) + ((size_t)page * s.Hkv + h) * bs * kD + cv * 8;
+    float *scale_at = (val ? vs : ks) + (size_t)page * s.Hkv + h;
+    const float was = off > 0 ? *scale_at : 0.f;
+    const bool mean = !val && L;
+    unsigned top = 0;
+    Raw8<T> x0;                            // the run's first rows, kept
+    const bool has0 = rs < n;
+    if (has0) x0.load(src + (off + rs) * ts);
+    uint2 old[NB];
+    if (mean) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            if (rs + RS * k < off) old[k] = *reinterpret_cast<const uint2 *>(blk + (size_t)(rs + RS * k) * kD);
+    }
+    int b = 0, pos = -1;
+    if (mean) {
+        const int i = (int)i0, last = cu[s.B];
+        b = warp_owner(cu, s.B, min(i, last - 1));
+        if (i < last) pos = new_len[b] - cu[b + 1] + i;
+        if (pos < 0 || pos % bs != off || pos / bs >= s.maxb) {
+            if (lane == 0) set_status(status, kStatusBadIndex);
+            pos = -1;
+        }
+    }
+    if (has0) top = x0.top();
+#pragma unroll 4
+    for (int r = rs + RS; r < n; r += RS) {
+        Raw8<T> z;
+        z.load(src + (off + r) * ts);
+        top = max(top, z.top());
+    }
+    top = __reduce_max_sync(~0u, top);
+    const bool odd = top >= 0x7f800000u;
+    if (odd) {
+        // not all finite: the largest of those that are
+        if (lane == 0) set_status(status, kStatusNaN);
+        top = 0;
+        for (int r = rs; r < n; r += RS) {
+            Raw8<T> z;
+            z.load(src + (off + r) * ts);
+            float f[8];
+            z.get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned u = __float_as_uint(f[e]) & 0x7fffffffu;
+                top = max(top, u < 0x7f800000u ? u : 0u);
+            }
+        }
+        top = __reduce_max_sync(~0u, top);
+    }
+    const float am = __uint_as_float(top);
+    const bool usable = was >= 1.17549435e-38f && was <= 3.402823466e38f;
+    const bool fits = off > 0 && usable && am <= kMost * was;
+    const float now = fits ? was : scale_for<kCode>(am);
+    Sum8<kCode> sum;
+    sum.zero();
+    if (!fits) {
+        const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
+#pragma unroll 1
+        for (int r = rs; r < off; r += RS) {
+            uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD), c = *at;
+            float y[8];
+            code_values4<kCode>(c.x, y);
+            code_values4<kCode>(c.y, y + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= ratio;
+            c = encode8<kCode>(y, 1.f);
+            *at = c;
+            if (mean) sum.add(c);
+        }
+    } else if (mean) {
+        for (int k0 = 0; k0 * RS < off; k0 += NB) {
+            uint2 nx[NB];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int r = rs + RS * (k0 + NB + k);
+                if (r < off) nx[k] = *reinterpret_cast<const uint2 *>(blk + (size_t)r * kD);
+            }
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                if (rs + RS * (k0 + k) < off) sum.add(old[k]);
+                old[k] = nx[k];
+            }
+        }
+    }
+    const bool pow2 = !odd && (__float_as_uint(now) & 0x7fffffu) == 0;
+    const float inv = __fdiv_rn(1.f, now);
+#pragma unroll 4
+    for (int r = rs; r < n; r += RS) {
+        Raw8<T> z = x0;
+        if (r >= RS) z.load(src + (off + r) * ts);
+        float y[8];
+        z.get(y);
+        const uint2 c = pow2 ? encode8<kCode>(y, inv) : encode8_any<kCode>(y, now);
+        *reinterpret_cast<uint2 *>(blk + (size_t)(off + r) * kD) = c;
+        if (mean) sum.add(c);
+    }
+    if (lane == 0) *scale_at = now;
+    if (mean) {
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            acc[e] = sum.get(e);
+#pragma unroll
+            for (int o = VPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(~0u, acc[e], o);
+            acc[e] = __fdiv_rn(acc[e] * now, (float)(off + n));
+        }
+        if (pos >= 0 && lane < VPR) {
+            T *to = L + (((size_t)b * s.Hkv + h) * s.maxb + pos / bs) * kD + cv * 8;
+#pragma unroll
+            for (int e = 0; e < 8; e += Vec<T>::n) store16(to + e, acc + e);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Read-back: row i = the cached keys and values at slot[i] (zeros where the
 // slot is negative or out of range).  One thread per 16 codes of K and of V.
@@ -539,10 +698,19 @@ template <typename T, int kCode>
 cudaError_t append_t(const PagedShape &s, const void *K, const void *V, long long ts, long long hs,
                      const int64_t *slot, const int32_t *cu, const int32_t *nl, uint8_t *K8, uint8_t *V8, float *ks,
                      float *vs, void *L, unsigned *status, cudaStream_t st) {
-    // One token per CTA while the CTAs of all (token, head) pairs fit about
-    // one wave of eight per SM (decode steps); longer windows beyond that, so
-    // that a prompt's tokens, of which one in `block` begins a run, do not
-    // cost a CTA each.
+    // While a warp per (token, head, keys or values) fits the GPU at once (64
+    // an SM), a call is a step of single tokens or as short as one: a warp
+    // each takes 256 tokens of 8 heads in 11 us, the windows below in 20.
+    if ((long long)s.tokens * s.Hkv * 2 <= 64ll * max(1, sm_count())) {
+        auto k = s.d == 128 ? paged_append_step_kernel<T, kCode, 128> : paged_append_step_kernel<T, kCode, 64>;
+        k<<<(unsigned)(((long long)s.tokens * s.Hkv * 2 + 3) / 4), 128, 0, st>>>(
+            s, (const T *)K, (const T *)V, ts, hs, slot, cu, nl, K8, V8, ks, vs, (T *)L, status);
+        note_launch();
+        return cudaGetLastError();
+    }
+    // Windows as long as leaves about a wave of eight CTAs per SM, so that a
+    // prompt's tokens, of which one in `block` begins a run, do not cost a CTA
+    // each.
     int window = 1;
     while (window < kWinMax && (long long)s.tokens * s.Hkv > (long long)window * 8 * max(1, sm_count())) window <<= 1;
     const unsigned grid = (unsigned)((s.tokens + window - 1) / window * s.Hkv * 2);

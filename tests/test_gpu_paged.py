@@ -199,6 +199,49 @@ def test_append_follows_the_oracle(code, dtype, d, block, Hkv):
 
 
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 64), ("bf16", 64, 128), ("fp32", 128, 80), ("bf16", 128, 16)])
+def test_append_of_long_prompts(code, dtype, d, block):
+    """Enough tokens that windows of several runs share a CTA, appended in two
+    calls of ragged prompts and single tokens, some of them not finite."""
+    rng = np.random.default_rng(block)
+    B, Hkv = 130, 2
+    grown = [[1] * B, [int(x) for x in rng.integers(0, 3, B)]]
+    grown[0][5], grown[0][60] = 1500, 3 * block
+    grown[1][5], grown[1][7], grown[1][61] = 2 * block + 5, 700, block - 1
+    maxb = 2300 // block + 3
+    lens = np.zeros(B, int)
+    pages = sum(-(-(a + b) // block) for a, b in zip(*grown)) + 1
+    p0 = sa.make_paged_params(B, Hkv, Hkv, d, block, pages, maxb, 0, code=code, dtype=dtype)
+    table = random_table(p0, [a + b for a, b in zip(*grown)], 3)
+    cache = sa.paged_cache(p0)
+    codes, scale = [raw(c) for c in cache[:2]], [np.zeros((pages, Hkv)) for _ in "kv"]
+    L = torch.zeros(B, Hkv, maxb, d, dtype=T[dtype], device="cuda")
+    for step, g in enumerate(grown):
+        lens = lens + np.array(g)
+        slot, cu = split_slots(p0, table, lens, g, pad=2600)
+        n = len(slot)
+        x = [torch.from_numpy(rng.standard_normal((n, Hkv, d)) * 2.0 ** (step - 2)).to(T[dtype]) for _ in "kv"]
+        x[0][7, 1, 3], x[1][200, 0, 0], x[1][201, 0, 1] = math.inf, math.nan, -math.inf
+        p = sa.make_paged_params(B, Hkv, Hkv, d, block, pages, maxb, n, code=code, dtype=dtype)
+        assert n * Hkv * 2 > 64 * 148          # one warp a token no longer
+        ws = sa.paged_workspace(p, ops=[sa.SA_OP_PAGED_APPEND])
+        sa.paged_append(p, x[0].cuda(), x[1].cuda(), torch.tensor(slot, device="cuda"), cache, ws, cu=i32(cu),
+                        new_len=i32(lens.tolist()), L=L)
+        torch.cuda.synchronize()
+        assert sa.sparse_attn_check_status(ws.data_ptr(), 0) == (sa.SA_ERR_DEVICE, 2)
+        for i in range(2):
+            op.append(CODE[code], block, x[i].double().numpy(), slot, codes[i], scale[i])
+            assert np.array_equal(raw(cache[i]), codes[i]), (step, i)
+            assert np.array_equal(cache[2 + i].double().cpu().numpy(), scale[i]), (step, i)
+    vals = op.values(CODE[code], codes[0], scale[0])
+    for b in (0, 5, 7, 60, 61, 129):
+        for j in range(-(-int(lens[b]) // block)):
+            ref = vals[table[b, j], :, :min(block, lens[b] - j * block)].mean(1)
+            tol = (torch.finfo(T[dtype]).eps / 2 + 3 * 2.0 ** -24) * np.abs(ref) + 2.0 ** -24 * (448 if code == "e4m3" else 127) * scale[0].max()
+            assert (np.abs(L[b, :, j].double().cpu().numpy() - ref) <= tol).all(), (b, j)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
 def test_append_of_what_is_not_finite(code):
     p = sa.make_paged_params(1, 1, 1, 64, 16, 2, 2, 3, code=code)
     cache, ws = sa.paged_cache(p), sa.paged_workspace(p)
