@@ -95,11 +95,14 @@ struct PagedLists {
 cudaError_t launch_paged_simt(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
                               const PagedLists &l, void *o, float *lse, unsigned *status, cudaStream_t st);
 
-// The tensor-core decode: bf16, `scratch` of paged_decode_scratch bytes.
+// The tensor-core decode: bf16, `scratch` of paged_decode_scratch bytes.  With
+// cu it takes packed chunks of few rows (paged_rows_supported; no lists).
 bool paged_decode_supported(const PagedShape &s);
-size_t paged_decode_scratch(const PagedShape &s);
-cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
-                                float *lse, unsigned *status, void *scratch, cudaStream_t st);
+bool paged_rows_supported(const PagedShape &s);
+size_t paged_decode_scratch(const PagedShape &s, bool chunk);
+cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
+                                const PagedLists &l, void *o, float *lse, unsigned *status, void *scratch,
+                                cudaStream_t st);
 // The tensor-core chunk attention: bf16, up to 128 query heads per kv-head.
 bool paged_prefill_supported(const PagedShape &s);
 size_t paged_prefill_scratch(const PagedShape &s);

@@ -79,9 +79,12 @@ size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op) {
         case SA_OP_PAGED_TABLES:
         case SA_OP_PAGED_APPEND:
         case SA_OP_PAGED_GATHER: return kStatusBytes;
-        case SA_OP_PAGED_DECODE: return kStatusBytes + al256(paged_decode_scratch(s));
+        case SA_OP_PAGED_DECODE: return kStatusBytes + al256(paged_decode_scratch(s, false));
         case SA_OP_PAGED_PREFILL:
-            return kStatusBytes + (s.tokens > 0 && paged_prefill_supported(s) ? al256(paged_prefill_scratch(s)) : 0);
+            return kStatusBytes + al256(s.tokens == 0                ? 0
+                                        : paged_rows_supported(s)    ? paged_decode_scratch(s, true)
+                                        : paged_prefill_supported(s) ? paged_prefill_scratch(s)
+                                                                     : 0);
         default: return 0;
     }
 }
@@ -151,7 +154,7 @@ int sparse_attn_paged_decode(const sa_paged_params *p, const void *q, const void
     const PagedCache c{(const uint8_t *)K8, (const uint8_t *)V8, kscale, vscale, table, seq_len};
     const PagedLists l{idx, score, count};
     if (paged_decode_supported(s))
-        return launch_result(launch_paged_decode(s, q, c, l, o, lse, (unsigned *)ws,
+        return launch_result(launch_paged_decode(s, q, nullptr, c, l, o, lse, (unsigned *)ws,
                                                  (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
     return launch_result(launch_paged_simt(s, q, nullptr, c, l, o, lse, (unsigned *)ws, (cudaStream_t)stream));
 }
@@ -169,6 +172,9 @@ int sparse_attn_paged_prefill(const sa_paged_params *p, const void *Q, const int
     if (ws_bytes < sparse_attn_paged_workspace_size(p, SA_OP_PAGED_PREFILL)) return SA_ERR_WORKSPACE;
     if (s.tokens == 0) return SA_OK;
     const PagedCache c{(const uint8_t *)K8, (const uint8_t *)V8, kscale, vscale, table, seq_len};
+    if (paged_rows_supported(s))
+        return launch_result(launch_paged_decode(s, Q, cu, c, PagedLists{}, O, lse, (unsigned *)ws,
+                                                 (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
     if (paged_prefill_supported(s))
         return launch_result(launch_paged_prefill(s, Q, cu, c, O, lse, (unsigned *)ws,
                                                   (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));

@@ -47,7 +47,6 @@ template <int kNT>
 constexpr int warps_of() { return kNT == 1 ? 12 : 8; }
 constexpr int kMaxWarps = 12;
 constexpr int kMinRange = 2;   // stages: shorter ranges cost more in records than they save
-constexpr int kMergeWarps = 8;
 // stage flags: first / last stage of its unit in this range, the unit lies in
 // this range as a whole, it begins before this range, some keys are not there
 enum { F_NEW = 1, F_LAST = 2, F_WHOLE = 4, F_CUT = 8, F_TAIL = 16 };
@@ -62,7 +61,9 @@ struct DecArgs {
     unsigned *status;
     int2 *info;          // [units] first range, ranges (0: nothing to join)
     float *rec;          // [ranges][2] records
-    int units, hg;       // units = B * Hsel * hg; hg head groups per list
+    const int32_t *cu;   // packed chunk rows, or null: one query per sequence
+    int units, hg;       // units = B * Hsel * hg; hg groups of query rows per list
+    int group;           // rows per group
     int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
 };
 
@@ -125,12 +126,15 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
     return kD == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Where a unit lies: its list, batch and heads.
+// Where a unit lies: its list, and rows r0 .. r0 + rn - 1 of those that read
+// it.  They are the query heads of the list, or with a chunk its tokens times
+// the group's heads, token-major.
 struct UnitAt {
-    int b, g, h0, hn;      // heads h0 .. h0 + hn - 1
+    int b, g, r0, rn;
+    int head0;             // decode: first query head of the list; chunk: of the group
+    int first, T;          // chunk: first packed row and tokens of the sequence
     size_t lu;             // list row
 };
-template <int kNT>
 __device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int u) {
     const PagedShape &s = a.s;
     UnitAt w;
@@ -139,19 +143,44 @@ __device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int u) {
     w.b = lu / s.Hsel;
     w.lu = (size_t)lu;
     const bool perq = s.flags & SA_SELECT_PER_QHEAD;
-    w.g = perq ? hs / s.G : hs;
-    w.h0 = (perq ? hs : hs * s.G) + grp * 16;
-    w.hn = min(8 * kNT, s.heads_per - grp * 16);
+    w.r0 = grp * a.group;
+    if (!a.cu) {
+        w.g = perq ? hs / s.G : hs;
+        w.head0 = perq ? hs : hs * s.G;
+        w.first = w.T = 0;
+        w.rn = min(a.group, s.heads_per - w.r0);
+    } else {
+        w.g = hs;
+        w.head0 = hs * s.G;
+        w.first = max(0, min(a.cu[w.b], s.tokens));
+        w.T = max(w.first, min(a.cu[w.b + 1], s.tokens)) - w.first;
+        w.rn = (int)min((long long)a.group, (long long)w.T * s.G - w.r0);
+    }
     return w;
 }
+// Row of q, o and lse that the unit's row i is, and the keys it sees.
+__device__ __forceinline__ size_t row_at(const DecArgs &a, const UnitAt &w, int i) {
+    if (!a.cu) return (size_t)w.b * a.s.Hq + w.head0 + w.r0 + i;
+    const int t = (w.r0 + i) / a.s.G;
+    return (size_t)(w.first + t) * a.s.Hq + w.head0 + (w.r0 + i - t * a.s.G);
+}
+__device__ __forceinline__ int sees(const DecArgs &a, const UnitAt &w, int n, int i) {
+    return !a.cu || !(a.s.flags & SA_CAUSAL) ? n : n - w.T + (w.r0 + i) / a.s.G + 1;
+}
 
-// Entries (blocks) of a unit: its list's, or every block of its sequence.
+// Entries (blocks) of a unit: its list's, or every block that one of its rows
+// sees.
 __device__ __forceinline__ int entries_of(const DecArgs &a, int u) {
     const int lu = u / a.hg;
     const int listed = a.l.idx ? a.l.count[lu] : 0;     // both loads in flight
-    const int n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
-    if (!a.l.idx) return (n + a.s.bs - 1) / a.s.bs;
-    return n > 0 ? max(0, min(listed, a.s.cap)) : 0;
+    int n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
+    if (a.l.idx) return n > 0 ? max(0, min(listed, a.s.cap)) : 0;
+    if (a.cu) {
+        const UnitAt w = unit_at(a, u);
+        if (w.rn <= 0) return 0;
+        n = max(0, min(n, sees(a, w, n, w.rn - 1)));
+    }
+    return (n + a.s.bs - 1) / a.s.bs;
 }
 __device__ __forceinline__ int stages_of(const DecArgs &a, int entries) {
     return (entries * a.sub + a.pps - 1) / a.pps;
@@ -199,39 +228,14 @@ struct Acc {
             r[32 * i++ + lane] = l[k];
         }
     }
-    // joins a saved record (same lane layout)
-    __device__ __forceinline__ void join(const float *r, int lane) {
-        constexpr int no = kD / 16 * kNT * 4;
-        float x[no];
-#pragma unroll
-        for (int i = 0; i < no; ++i) x[i] = r[32 * i + lane];
-        float fa[2 * kNT], fb[2 * kNT];
-#pragma unroll
-        for (int k = 0; k < 2 * kNT; ++k) {
-            const float m2 = r[32 * (no + 2 * k) + lane], l2 = r[32 * (no + 2 * k + 1) + lane];
-            const float M = fmaxf(m[k], m2);
-            fa[k] = m[k] == -CUDART_INF_F ? 0.f : ex2(m[k] - M);
-            fb[k] = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - M);
-            l[k] = l[k] * fa[k] + l2 * fb[k];
-            m[k] = M;
-        }
-        int i = 0;
-#pragma unroll
-        for (int t = 0; t < kD / 16; ++t)
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e, ++i)
-                    o[t][n][e] = o[t][n][e] * fa[2 * n + (e & 1)] + x[i] * fb[2 * n + (e & 1)];
-    }
     __device__ __forceinline__ void store(const DecArgs &a, const UnitAt &w, int lane) const {
         const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
         for (int k = 0; k < 2 * kNT; ++k) {
             const int h = 8 * (k >> 1) + 2 * tq + (k & 1);
-            if (h >= w.hn) continue;
+            if (h >= w.rn) continue;
             const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
-            const size_t row = (size_t)w.b * a.s.Hq + w.h0 + h;
+            const size_t row = row_at(a, w, h);
             __nv_bfloat16 *dst = a.o + row * kD + 2 * gq;
 #pragma unroll
             for (int t = 0; t < kD / 16; ++t)
@@ -294,10 +298,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             n += stages_of(a, e);
             if (e == 0 && u % gridDim.x == blockIdx.x) {
                 // nothing kept: zeros
-                const UnitAt w = unit_at<kNT>(a, u);
+                const UnitAt w = unit_at(a, u);
                 a.info[u] = make_int2(0, 0);
-                for (int h = 0; h < w.hn; ++h) {
-                    const size_t row = (size_t)w.b * s.Hq + w.h0 + h;
+                for (int h = 0; h < w.rn; ++h) {
+                    const size_t row = row_at(a, w, h);
                     for (int i = 0; i < kD; i += 8)
                         *reinterpret_cast<uint4 *>(a.o + row * kD + i) = make_uint4(0, 0, 0, 0);
                     a.lse[row] = -CUDART_INF_F;
@@ -365,7 +369,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     };
     // steps 1 to 3, one dependent load each
     auto more = [&](Batch &t) {
-        const UnitAt w = unit_at<kNT>(a, t.unit);
+        const UnitAt w = unit_at(a, t.unit);
         if (t.step == 1) {
             const int c = t.s0 * a.pps + lane, e = c / a.sub;
             t.page = -1;
@@ -414,7 +418,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // The batch being issued (its records are in shared memory) and the one
     // being loaded behind it, whose last step waits until it takes over.
     Batch nxt;
-    int cu_unit = -1, cu_n = 0, cu_flags = 0, ci = 0;   // unit, stages, flags, stages issued
+    int cu_unit = -1, cu_s0 = 0, cu_n = 0, cu_flags = 0, ci = 0;   // unit, first stage, stages, flags, stages issued
     const uint32_t kb = smem_u32(sm) + warp * 2 * kHalfBytes, vb = kb + kHalfBytes;
     const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
     const uint32_t part_bytes = (uint32_t)a.rows * kD;
@@ -424,7 +428,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // scores, its values once that one has used its own, so one stage of
     // memory keeps one load in flight behind the arithmetic.
     uint32_t n_bytes = 0;
-    int n_flags = 0, n_unit = 0, n_first = 0;   // flags, unit and first part (with the batch's half) of that stage
+    // flags, unit, first part (with the batch's half) and first key of that stage
+    int n_flags = 0, n_unit = 0, n_first = 0, n_key = 0;
     auto issue_k = [&]() -> bool {              // false: the range is issued
         const bool fresh = ci == cu_n;
         if (fresh) {
@@ -432,6 +437,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             ++batch;
             while (nxt.step < 4) more(nxt);
             cu_unit = nxt.unit;
+            cu_s0 = nxt.s0;
             cu_n = nxt.s1 - nxt.s0;
             cu_flags = nxt.flags;
             ci = 0;
@@ -442,6 +448,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         n_bytes = part_bytes * __popc(__ballot_sync(~0u, live));
         n_first = 32 * (batch & 1) + first;
         n_unit = cu_unit;
+        if (a.cu) {
+            // every block in order: where the stage's keys lie, and whether
+            // the unit's first row sees them all
+            const int c = (cu_s0 + ci) * a.pps;
+            n_key = c / a.sub * s.bs + c % a.sub * a.rows;
+        }
         n_flags = (cu_flags & (F_WHOLE | F_CUT)) | (ci == 0 ? cu_flags & F_NEW : 0) |
                   (ci == cu_n - 1 ? cu_flags & F_LAST : 0) |
                   (__any_sync(~0u, lane < a.pps && at.nk < (kSingle ? 64 : a.rows)) ? F_TAIL : 0);
@@ -476,26 +488,33 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     Acc<kD, kNT> acc;
     uint32_t qb[kD / 16][kNT][2];
     float qf[2 * kNT];
+    int lim[2 * kNT], lim0 = 0;        // chunk: keys that the lane's rows see, that the unit's first row sees
     int done = 0;
     // v_out: this stage's values are on their way; k_next: the next one's keys
     bool ok = true, have = issue_k(), v_out = have, k_next = false;
     if (have) issue_v();
     for (; have; ++done) {
-        const int flags = n_flags, unit = n_unit;
+        const int flags = n_flags, unit = n_unit, key0 = n_key;
         const Part *part = &parts[warp][0][n_first];
         if (flags & F_NEW) {
             // the unit's queries: dimensions 16 k + 4 tq + {0, 1}, {2, 3} of head 8 n + gq
-            const UnitAt w = unit_at<kNT>(a, unit);
+            const UnitAt w = unit_at(a, unit);
             acc.reset();
+            if (a.cu) {
+                const int n = paged_len(s, a.c.seq_len, w.b);
+                lim0 = sees(a, w, n, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * kNT; ++i) lim[i] = sees(a, w, n, 8 * (i >> 1) + 2 * tq + (i & 1));
+            }
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
                 const int h = 8 * n + gq;
-                const __nv_bfloat16 *src = a.q + ((size_t)w.b * s.Hq + w.h0 + (h < w.hn ? h : 0)) * kD + 4 * tq;
+                const __nv_bfloat16 *src = a.q + row_at(a, w, h < w.rn ? h : 0) * kD + 4 * tq;
                 uint2 x[kD / 16];
                 unsigned big = 0;      // largest magnitude's bits
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
-                    x[k] = h < w.hn ? *reinterpret_cast<const uint2 *>(src + 16 * k) : make_uint2(0, 0);
+                    x[k] = h < w.rn ? *reinterpret_cast<const uint2 *>(src + 16 * k) : make_uint2(0, 0);
                     const unsigned y = __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
                     big = __vmaxu2(big, y);
                 }
@@ -558,16 +577,32 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const Part pt = part[t >> psh];
-            const int nk = pt.nk - 16 * (t & pmask);
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = fmaf(z[t][n][e], qf[2 * n + (e & 1)] * pt.ks, hier ? 0.f : pt.gate);
-                    z[t][n][e] = gq + 8 * (e >> 1) < nk ? x : -CUDART_INF_F;
-                    top[2 * n + (e & 1)] = fmaxf(top[2 * n + (e & 1)], z[t][n][e]);
-                }
+                for (int e = 0; e < 4; ++e)
+                    z[t][n][e] = fmaf(z[t][n][e], qf[2 * n + (e & 1)] * pt.ks, hier ? 0.f : pt.gate);
         }
+        if ((flags & F_TAIL) || (a.cu && key0 + 64 > lim0)) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int nk = part[t >> psh].nk - 16 * (t & pmask), k0 = key0 + 16 * t;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int k = gq + 8 * (e >> 1);
+                        const bool on = k < nk && (!a.cu || k0 + k < lim[2 * n + (e & 1)]);
+                        z[t][n][e] = on ? z[t][n][e] : -CUDART_INF_F;
+                    }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[2 * n + (e & 1)] = fmaxf(top[2 * n + (e & 1)], z[t][n][e]);
         float pf[2 * kNT];     // hierarchical: weight of the block over its sum
         if (!hier) {
             bool high = false;
@@ -717,7 +752,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 8);
                 acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 16);
             }
-            if (flags & F_WHOLE) acc.store(a, unit_at<kNT>(a, unit), lane);
+            if (flags & F_WHOLE) acc.store(a, unit_at(a, unit), lane);
             else acc.save(a.rec + ((size_t)range * 2 + (flags & F_CUT ? 0 : 1)) * rec_floats<kD, kNT>(), lane);
         }
     }
@@ -731,28 +766,122 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
 }
 
-// Joins the records of the units that several ranges shared: warp w takes
-// records w, w + kMergeWarps, ..., then the warps' states are joined in order.
-template <int kD, int kNT>
-__global__ void __launch_bounds__(32 * kMergeWarps)
+// Joins the records of the units that several ranges shared, in their order.
+// A warp takes an eighth of the lanes' values (and every row's max and sum) of
+// its group's share of the records, four records at a time; groups meet in
+// shared memory.  One group of 256 threads while there are more units than
+// SMs (few records each), three where few units have many records.
+constexpr int kSlices = 8, kBatch = 4;
+template <int kD, int kNT, int kGroups>
+__global__ void __launch_bounds__(32 * kSlices * kGroups)
 paged_merge_kernel(DecArgs a) {
-    __shared__ float part[kMergeWarps / 2][rec_floats<kD, kNT>()];
-    const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int NO = kD / 16 * kNT * 4, K = NO / kSlices, H = 2 * kNT;
+    __shared__ float part[kGroups > 1 ? kGroups - 1 : 1][kSlices][K + 2 * H][32];
+    const int u = blockIdx.x, lane = threadIdx.x & 31, slice = (threadIdx.x >> 5) % kSlices;
+    const int grp = threadIdx.x / (32 * kSlices), i0 = slice * K;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 in = a.info[u];
     if (in.y < 2) return;
-    Acc<kD, kNT> acc;
-    acc.reset();
-    for (int i = warp; i < in.y; i += kMergeWarps)
-        acc.join(a.rec + ((size_t)(in.x + i) * 2 + (i == 0 ? 1 : 0)) * rec_floats<kD, kNT>(), lane);
+    // the entry of the lane's rows that value k of the slice belongs to (a
+    // slice is whole tiles of 4 kNT values, or at d = 64 a part of one)
+    auto pick = [&](const float *f, int k) {
+        if constexpr (K >= 4 * kNT || kNT == 1) return f[2 * (k / 4 % kNT) + (k & 1)];
+        else return (slice * K / 4) % kNT ? f[2 + (k & 1)] : f[k & 1];
+    };
+    float m[H], l[H], o[K];
 #pragma unroll
-    for (int n = kMergeWarps / 2; n > 0; n >>= 1) {
-        if (warp >= n && warp < 2 * n) acc.save(part[warp - n], lane);
-        __syncthreads();
-        if (warp < n) acc.join(part[warp], lane);
-        __syncthreads();
+    for (int h = 0; h < H; ++h) {
+        m[h] = -CUDART_INF_F;
+        l[h] = 0.f;
     }
-    if (warp == 0) acc.store(a, unit_at<kNT>(a, u), lane);
+#pragma unroll
+    for (int k = 0; k < K; ++k) o[k] = 0.f;
+    const int share = (in.y + kGroups - 1) / kGroups, r0 = grp * share, r1 = min(in.y, r0 + share);
+    for (int r = r0; r < r1; r += kBatch) {
+        float xm[kBatch][H], xl[kBatch][H], xo[kBatch][K];
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            if (r + c >= r1) continue;
+            const float *p = a.rec + ((size_t)(in.x + r + c) * 2 + (r + c == 0 ? 1 : 0)) * rec_floats<kD, kNT>() + lane;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                xm[c][h] = p[32 * (NO + 2 * h)];
+                xl[c][h] = p[32 * (NO + 2 * h + 1)];
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) xo[c][k] = p[32 * (i0 + k)];
+        }
+        float f[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float M = m[h];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c)
+                if (r + c < r1) M = fmaxf(M, xm[c][h]);
+            f[h] = m[h] == -CUDART_INF_F ? 0.f : ex2(m[h] - M);
+            m[h] = M;
+            l[h] *= f[h];
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) o[k] *= pick(f, k);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            if (r + c >= r1) continue;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                f[h] = xm[c][h] == -CUDART_INF_F ? 0.f : ex2(xm[c][h] - m[h]);
+                l[h] += xl[c][h] * f[h];
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) o[k] += xo[c][k] * pick(f, k);
+        }
+    }
+    if constexpr (kGroups > 1) {
+        if (grp) {
+            float(*p)[32] = part[grp - 1][slice];
+#pragma unroll
+            for (int k = 0; k < K; ++k) p[k][lane] = o[k];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                p[K + 2 * h][lane] = m[h];
+                p[K + 2 * h + 1][lane] = l[h];
+            }
+        }
+        __syncthreads();
+        if (grp) return;
+#pragma unroll
+        for (int c = 0; c < kGroups - 1; ++c) {
+            const float(*p)[32] = part[c][slice];
+            float fa[H], fb[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float m2 = p[K + 2 * h][lane], l2 = p[K + 2 * h + 1][lane], M = fmaxf(m[h], m2);
+                fa[h] = m[h] == -CUDART_INF_F ? 0.f : ex2(m[h] - M);
+                fb[h] = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - M);
+                l[h] = l[h] * fa[h] + l2 * fb[h];
+                m[h] = M;
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) o[k] = o[k] * pick(fa, k) + p[k][lane] * pick(fb, k);
+        }
+    }
+    const UnitAt w = unit_at(a, u);
+    const int gq = lane >> 2, tq = lane & 3;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = i0 + k, row = 8 * (i / 4 % kNT) + 2 * tq + (i & 1);
+        const float lk = pick(l, k);
+        if (row < w.rn)
+            a.o[row_at(a, w, row) * kD + 16 * (i / (4 * kNT)) + 2 * gq + (i >> 1 & 1)] =
+                __float2bfloat16_rn(lk == 0.f ? 0.f : o[k] / lk);
+    }
+    if (slice == 0 && gq == 0) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int row = 8 * (h >> 1) + 2 * tq + (h & 1);
+            if (row < w.rn) a.lse[row_at(a, w, row)] = l[h] == 0.f ? -CUDART_INF_F : (m[h] + log2f(l[h])) * kLn2;
+        }
+    }
 }
 
 // Rows of codes [rows][d], one byte each, read in boxes of box_rows rows.
@@ -768,9 +897,24 @@ bool code_map(CUtensorMap *map, const uint8_t *base, uint64_t rows, int d, int b
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int head_tiles(const PagedShape &s) { return s.heads_per <= 8 ? 1 : 2; }
-int head_groups(const PagedShape &s) { return (s.heads_per + 15) / 16; }
-size_t rec_bytes(const PagedShape &s) { return (size_t)(s.d / 16 * 4 + 4) * head_tiles(s) * 32 * sizeof(float); }
+// Rows that read one list: the heads of a decode, or on average those of a
+// chunk (the packed rows know no more on the host).
+long long rows_per_list(const PagedShape &s, bool chunk) {
+    return chunk ? ((long long)s.tokens * s.G + s.B - 1) / s.B : s.heads_per;
+}
+int head_tiles(const PagedShape &s, bool chunk) { return rows_per_list(s, chunk) <= 8 ? 1 : 2; }
+// Groups of rows a list can have: with a chunk all its rows may be of one sequence.
+long long row_groups(const PagedShape &s, bool chunk) {
+    const int group = chunk ? 8 * head_tiles(s, true) : 16;
+    const long long most = chunk ? (long long)s.tokens * s.G : s.heads_per;
+    return (most + group - 1) / group;
+}
+long long units_of(const PagedShape &s, bool chunk) {
+    return (long long)s.B * (chunk ? s.Hkv : s.Hsel) * row_groups(s, chunk);
+}
+size_t rec_bytes(const PagedShape &s, bool chunk) {
+    return (size_t)(s.d / 16 * 4 + 4) * head_tiles(s, chunk) * 32 * sizeof(float);
+}
 // The workspace counts the 148 SMs of a B200; the grid follows the device.
 constexpr int kMaxGrid = 148;
 
@@ -783,7 +927,8 @@ cudaError_t run(const DecArgs &a, int grid, const CUtensorMap &mk, const CUtenso
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(32 * warps_of<kNT>()), smem, st, mk, mv, a);
     note_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_merge_kernel<kD, kNT>, dim3((unsigned)a.units), dim3(32 * kMergeWarps), 0, st, a);
+    e = a.units > grid ? launch_pdl(paged_merge_kernel<kD, kNT, 1>, dim3((unsigned)a.units), dim3(32 * kSlices), 0, st, a)
+                       : launch_pdl(paged_merge_kernel<kD, kNT, 3>, dim3((unsigned)a.units), dim3(96 * kSlices), 0, st, a);
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -795,23 +940,43 @@ bool paged_decode_supported(const PagedShape &s) {
     return s.dtype == SA_BF16 && !((s.flags & SA_HIER) && s.bs > 64);
 }
 
-size_t paged_decode_scratch(const PagedShape &s) {
-    const size_t units = (size_t)s.B * s.Hsel * head_groups(s);
-    return ((units * sizeof(int2) + 255) & ~(size_t)255) + (size_t)kMaxGrid * kMaxWarps * 2 * rec_bytes(s);
+// A chunk of few rows reads the cache once per 16 of them here, at the decode's
+// rate; the tiles of paged_prefill.cu take 256 rows in about twice the time of
+// one pass, so up to some 40 rows a sequence are better off here (8 sequences
+// of 5000 keys with 20 rows per kv-head: ... us against 56).  The units of the
+// step line must stay few enough for every CTA to look through.
+bool paged_rows_supported(const PagedShape &s) {
+    return s.dtype == SA_BF16 && s.tokens > 0 && rows_per_list(s, true) <= 40 && units_of(s, true) <= 16384;
 }
 
-cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedCache &c, const PagedLists &l, void *o,
-                                float *lse, unsigned *status, void *scratch, cudaStream_t st) {
+size_t paged_decode_scratch(const PagedShape &s, bool chunk) {
+    return ((units_of(s, chunk) * sizeof(int2) + 255) & ~(size_t)255) +
+           (size_t)kMaxGrid * kMaxWarps * 2 * rec_bytes(s, chunk);
+}
+
+cudaError_t launch_paged_decode(const PagedShape &shape, const void *q, const int32_t *cu, const PagedCache &c,
+                                const PagedLists &l, void *o, float *lse, unsigned *status, void *scratch,
+                                cudaStream_t st) {
+    PagedShape s = shape;
+    const bool chunk = cu != nullptr;
+    if (chunk) {
+        // no lists: a kv-head's rows go together
+        s.flags &= SA_CAUSAL;
+        s.Hsel = s.Hkv;
+        s.heads_per = s.G;
+    }
     DecArgs a{};
     a.s = s;
     a.c = c;
     a.l = l;
+    a.cu = cu;
     a.q = (const __nv_bfloat16 *)q;
     a.o = (__nv_bfloat16 *)o;
     a.lse = lse;
     a.status = status;
-    a.hg = head_groups(s);
-    a.units = s.B * s.Hsel * a.hg;
+    a.hg = (int)row_groups(s, chunk);
+    a.group = chunk ? 8 * head_tiles(s, true) : 16;
+    a.units = (int)units_of(s, chunk);
     a.info = (int2 *)scratch;
     a.rec = (float *)((unsigned char *)scratch + (((size_t)a.units * sizeof(int2) + 255) & ~(size_t)255));
     // a page of up to 64 tokens is one part, a longer one two; small pages
@@ -826,7 +991,7 @@ cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const PagedC
     if (!code_map(&mk, c.K, rows, s.d, a.rows) || !code_map(&mv, c.V, rows, s.d, a.rows))
         return cudaErrorInvalidValue;
     const int grid = min(sms, kMaxGrid);
-    const int key = (s.d == 128 ? 4 : 0) | (s.code == SA_E4M3 ? 2 : 0) | (head_tiles(s) == 2 ? 1 : 0);
+    const int key = (s.d == 128 ? 4 : 0) | (s.code == SA_E4M3 ? 2 : 0) | (head_tiles(s, chunk) == 2 ? 1 : 0);
     switch (key) {
         case 0: return run<64, SA_INT8, 1>(a, grid, mk, mv, st);
         case 1: return run<64, SA_INT8, 2>(a, grid, mk, mv, st);

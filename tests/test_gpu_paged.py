@@ -438,8 +438,25 @@ def test_decode_magnitudes():
     ("int8", "bf16", 128, 48, 24, 2), ("e4m3", "bf16", 128, 16, 40, 1), ("int8", "fp32", 64, 64, 6, 2),
     ("int8", "bf16", 64, 64, 16, 2)])
 def test_prefill_chunks(causal, code, dtype, d, block, Hq, Hkv):
-    lens = [300, 0, 1, 257, 40, 600, 130]
     grown = [70, 0, 1, 257, 55, 3, 0]          # sequence 4: more queries than keys
+    run_chunks(causal, code, dtype, d, block, Hq, Hkv, grown)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("code,d,block,Hq,Hkv,grown", [
+    ("e4m3", 128, 64, 8, 2, [5, 0, 1, 9, 7, 3, 0]), ("int8", 128, 128, 4, 4, [12, 0, 1, 3, 2, 30, 0]),
+    ("e4m3", 64, 16, 5, 1, [3, 0, 1, 2, 8, 1, 1]), ("int8", 64, 48, 24, 2, [1, 0, 1, 4, 1, 2, 0]),
+    ("e4m3", 128, 112, 40, 1, [2, 0, 1, 1, 1, 1, 0]), ("int8", 128, 32, 4, 4, [1, 0, 1, 1, 1, 1, 1])])
+def test_prefill_of_few_rows(causal, code, d, block, Hq, Hkv, grown):
+    """Drafted tokens: few rows per list, some of them in one long run."""
+    run_chunks(causal, code, "bf16", d, block, Hq, Hkv, grown)
+
+
+def run_chunks(causal, code, dtype, d, block, Hq, Hkv, grown):
+    lens = [300, 0, 1, 257, 40, 600, 130]
+    grown = list(grown)
+    if grown[4] < 30:
+        lens[4] = grown[4] - 1                 # more queries than keys
     if not causal:
         grown[1] = 2                           # queries of a sequence without keys
     maxb = 600 // block + 2
