@@ -59,10 +59,10 @@ struct DecArgs {
     __nv_bfloat16 *o;
     float *lse;
     unsigned *status;
-    int2 *info;          // [units] first range, ranges (0: nothing to join)
+    int4 *info;          // [units] first range, ranges (0: nothing to join), list, group
     float *rec;          // [ranges][2] records
     const int32_t *cu;   // packed chunk rows, or null: one query per sequence
-    int units, hg;       // units = B * Hsel * hg; hg groups of query rows per list
+    int lists, units;    // B * Hsel lists; the most units (groups of a list's rows) there can be
     int group;           // rows per group
     int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
 };
@@ -126,60 +126,57 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
     return kD == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Where a unit lies: its list, and rows r0 .. r0 + rn - 1 of those that read
-// it.  They are the query heads of the list, or with a chunk its tokens times
-// the group's heads, token-major.
-struct UnitAt {
-    int b, g, r0, rn;
-    int head0;             // decode: first query head of the list; chunk: of the group
-    int first, T;          // chunk: first packed row and tokens of the sequence
-    size_t lu;             // list row
+// A list and the query rows that read it: the query heads of the list, or with
+// a chunk its tokens times the group's heads, token-major.
+struct ListAt {
+    int b, g, head0;       // head0: first query head of the list, or of the group
+    int n, listed;         // keys of the sequence, entries listed
+    int first, T, rows;    // chunk: first packed row, tokens; rows that read the list
 };
-__device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int u) {
+__device__ __forceinline__ ListAt list_at(const DecArgs &a, int lu) {
     const PagedShape &s = a.s;
-    UnitAt w;
-    const int grp = u % a.hg;
-    const int lu = u / a.hg, hs = lu % s.Hsel;
-    w.b = lu / s.Hsel;
-    w.lu = (size_t)lu;
+    ListAt w;
+    const int hs = lu % s.Hsel;
     const bool perq = s.flags & SA_SELECT_PER_QHEAD;
-    w.r0 = grp * a.group;
-    if (!a.cu) {
-        w.g = perq ? hs / s.G : hs;
-        w.head0 = perq ? hs : hs * s.G;
-        w.first = w.T = 0;
-        w.rn = min(a.group, s.heads_per - w.r0);
-    } else {
-        w.g = hs;
-        w.head0 = hs * s.G;
-        w.first = max(0, min(a.cu[w.b], s.tokens));
-        w.T = max(w.first, min(a.cu[w.b + 1], s.tokens)) - w.first;
-        w.rn = (int)min((long long)a.group, (long long)w.T * s.G - w.r0);
-    }
+    w.b = lu / s.Hsel;
+    w.listed = a.l.idx ? a.l.count[lu] : 0;     // all loads in flight
+    const int c0 = a.cu ? a.cu[w.b] : 0, c1 = a.cu ? a.cu[w.b + 1] : 0;
+    w.n = paged_len(s, a.c.seq_len, w.b);
+    w.g = perq ? hs / s.G : hs;
+    w.head0 = perq ? hs : hs * s.G;
+    w.first = max(0, min(c0, s.tokens));
+    w.T = max(w.first, min(c1, s.tokens)) - w.first;
+    w.rows = a.cu ? w.T * s.G : s.heads_per;
+    return w;
+}
+// A unit: a group of up to a.group rows of one list, r0 .. r0 + rn - 1.
+struct UnitAt {
+    ListAt l;
+    int r0, rn;
+};
+__device__ __forceinline__ UnitAt unit_at(const DecArgs &a, int lu, int grp) {
+    UnitAt w{list_at(a, lu), grp * a.group, 0};
+    w.rn = min(a.group, w.l.rows - w.r0);
     return w;
 }
 // Row of q, o and lse that the unit's row i is, and the keys it sees.
 __device__ __forceinline__ size_t row_at(const DecArgs &a, const UnitAt &w, int i) {
-    if (!a.cu) return (size_t)w.b * a.s.Hq + w.head0 + w.r0 + i;
+    if (!a.cu) return (size_t)w.l.b * a.s.Hq + w.l.head0 + w.r0 + i;
     const int t = (w.r0 + i) / a.s.G;
-    return (size_t)(w.first + t) * a.s.Hq + w.head0 + (w.r0 + i - t * a.s.G);
+    return (size_t)(w.l.first + t) * a.s.Hq + w.l.head0 + (w.r0 + i - t * a.s.G);
 }
-__device__ __forceinline__ int sees(const DecArgs &a, const UnitAt &w, int n, int i) {
-    return !a.cu || !(a.s.flags & SA_CAUSAL) ? n : n - w.T + (w.r0 + i) / a.s.G + 1;
+__device__ __forceinline__ int sees(const DecArgs &a, const ListAt &l, int r) {
+    return !a.cu || !(a.s.flags & SA_CAUSAL) ? l.n : l.n - l.T + r / a.s.G + 1;
+}
+__device__ __forceinline__ int groups_of(const DecArgs &a, const ListAt &l) {
+    return (l.rows + a.group - 1) / a.group;
 }
 
 // Entries (blocks) of a unit: its list's, or every block that one of its rows
 // sees.
-__device__ __forceinline__ int entries_of(const DecArgs &a, int u) {
-    const int lu = u / a.hg;
-    const int listed = a.l.idx ? a.l.count[lu] : 0;     // both loads in flight
-    int n = paged_len(a.s, a.c.seq_len, lu / a.s.Hsel);
-    if (a.l.idx) return n > 0 ? max(0, min(listed, a.s.cap)) : 0;
-    if (a.cu) {
-        const UnitAt w = unit_at(a, u);
-        if (w.rn <= 0) return 0;
-        n = max(0, min(n, sees(a, w, n, w.rn - 1)));
-    }
+__device__ __forceinline__ int entries_of(const DecArgs &a, const ListAt &l, int grp) {
+    if (a.l.idx) return l.n > 0 ? max(0, min(l.listed, a.s.cap)) : 0;
+    const int n = max(0, min(l.n, sees(a, l, min(l.rows, (grp + 1) * a.group) - 1)));
     return (n + a.s.bs - 1) / a.s.bs;
 }
 __device__ __forceinline__ int stages_of(const DecArgs &a, int entries) {
@@ -250,7 +247,7 @@ struct Acc {
 // so that the chain count -> list -> table -> scales is in flight behind the
 // stages before it.
 struct Batch {
-    int unit, entries;          // -1: none
+    int list, grp, entries;     // list -1: none
     int s0, s1;                 // stages of the unit
     int flags;                  // F_NEW: s0 is the unit's first stage here; F_LAST: s1 - 1 its last; F_WHOLE, F_CUT
     int step;                   // load steps done
@@ -276,50 +273,95 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     __shared__ uint64_t bars[kWarps][2];      // the warp's keys, its values
     __shared__ long long pre[kThreads + 1];
     __shared__ long long wtot[kWarps];
-    __shared__ volatile int abort_s;
+    __shared__ int preu[kThreads + 1], wtotu[kWarps];
+    __shared__ volatile int abort_s, bad_s;
     const PagedShape &s = a.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const bool hier = s.flags & SA_HIER;
     if (tid == 0) {
         for (int i = 0; i < kWarps * 2; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
         abort_s = 0;
+        bad_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
 
-    // ---- the line of stages: offsets of each thread's share of the units -----
-    const int share = (a.units + kThreads - 1) / kThreads;
+    // ---- the line of stages: offsets of each thread's share of the lists ------
+    const int share = (a.lists + kThreads - 1) / kThreads;
+    const int l0 = min(a.lists, tid * share), l1 = min(a.lists, l0 + share);
     {
-        const int u0 = min(a.units, tid * share), u1 = min(a.units, u0 + share);
         long long n = 0;
-        for (int u = u0; u < u1; ++u) {
-            const int e = entries_of(a, u);
-            n += stages_of(a, e);
-            if (e == 0 && u % gridDim.x == blockIdx.x) {
-                // nothing kept: zeros
-                const UnitAt w = unit_at(a, u);
-                a.info[u] = make_int2(0, 0);
-                for (int h = 0; h < w.rn; ++h) {
-                    const size_t row = row_at(a, w, h);
-                    for (int i = 0; i < kD; i += 8)
-                        *reinterpret_cast<uint4 *>(a.o + row * kD + i) = make_uint4(0, 0, 0, 0);
-                    a.lse[row] = -CUDART_INF_F;
-                }
+        int nu = 0;
+        bool none = false;        // a unit of this CTA's lists keeps nothing
+        for (int lu = l0; lu < l1; ++lu) {
+            const ListAt l = list_at(a, lu);
+            if (a.cu && !(a.cu[l.b] >= 0 && a.cu[l.b] <= a.cu[l.b + 1] && a.cu[l.b + 1] <= s.tokens)) bad_s = 1;
+            const int ng = groups_of(a, l);
+            for (int grp = 0; grp < ng; ++grp) {
+                const int e = entries_of(a, l, grp);
+                n += stages_of(a, e);
+                none |= e == 0 && lu % gridDim.x == blockIdx.x;
             }
+            nu += ng;
         }
         long long inc = n;
+        int incu = nu;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += y;
+            const int yu = __shfl_up_sync(~0u, incu, o);
+            if (lane >= o) {
+                inc += y;
+                incu += yu;
+            }
         }
-        if (lane == 31) wtot[warp] = inc;
+        if (lane == 31) {
+            wtot[warp] = inc;
+            wtotu[warp] = incu;
+        }
         __syncthreads();
-        for (int w = 0; w < warp; ++w) inc += wtot[w];
+        for (int w = 0; w < warp; ++w) {
+            inc += wtot[w];
+            incu += wtotu[w];
+        }
         pre[tid] = inc - n;
-        if (tid == kThreads - 1) pre[kThreads] = inc;
+        preu[tid] = incu - nu;
+        if (tid == kThreads - 1) {
+            pre[kThreads] = inc;
+            preu[kThreads] = incu;
+        }
         __syncthreads();
+        if (bad_s) {
+            // a chunk's offsets do not ascend within its rows: nothing is done
+            for (int id = blockIdx.x * kThreads + tid; id < a.units; id += gridDim.x * kThreads)
+                a.info[id] = make_int4(0, 0, 0, 0);
+            if (tid == 0) set_status(a.status, kStatusBadIndex);
+            return;
+        }
+        if (none) {
+            int id = incu - nu;
+            for (int lu = l0; lu < l1; ++lu) {
+                const ListAt l = list_at(a, lu);
+                const int ng = groups_of(a, l);
+                for (int grp = 0; grp < ng; ++grp, ++id) {
+                    if (entries_of(a, l, grp) > 0 || lu % gridDim.x != blockIdx.x) continue;
+                    // nothing kept: zeros
+                    a.info[id] = make_int4(0, 0, 0, 0);
+                    const UnitAt w = unit_at(a, lu, grp);
+                    for (int h = 0; h < w.rn; ++h) {
+                        const size_t row = row_at(a, w, h);
+                        for (int i = 0; i < kD; i += 8)
+                            *reinterpret_cast<uint4 *>(a.o + row * kD + i) = make_uint4(0, 0, 0, 0);
+                        a.lse[row] = -CUDART_INF_F;
+                    }
+                }
+            }
+        }
+        // units that this call does not have
+        for (int id = preu[kThreads] + blockIdx.x * kThreads + tid; id < a.units; id += gridDim.x * kThreads)
+            a.info[id] = make_int4(0, 0, 0, 0);
     }
     const long long total = pre[kThreads];
     const int ranges = gridDim.x * kWarps;
@@ -331,30 +373,41 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
     // ---- issue side ----------------------------------------------------------
     int batch = 1;                     // batches issued (records alternate between two places)
-    int bu;                            // unit of stage xi, and its first stage
-    long long bpu, xi = x0;            // xi: next stage to put in a batch
+    // The unit of stage xi, the next one to put in a batch: list, group, number
+    // in the call, and its first stage.
+    int wl, wg = 0, wid;
+    long long bpu, xi = x0;
     {
         int best = 0;
         for (int t = lane; t < kThreads; t += 32)
             if (pre[t] <= x0) best = t;
         best = __reduce_max_sync(~0u, best);
-        bu = best * share;
+        wl = best * share;
         bpu = pre[best];
+        wid = preu[best];
     }
+    ListAt wlist = list_at(a, wl);
     // step 0: unit and part of the line
     auto open = [&](Batch &t) {
         t.step = 0;
-        t.unit = -1;
+        t.list = -1;
         if (xi >= x1) return;
         int n;
         for (;;) {
-            t.entries = entries_of(a, bu);
+            if (wg == groups_of(a, wlist)) {
+                wg = 0;
+                wlist = list_at(a, ++wl);
+                continue;
+            }
+            t.entries = entries_of(a, wlist, wg);
             n = stages_of(a, t.entries);
             if (xi < bpu + n) break;
             bpu += n;
-            ++bu;
+            ++wg;
+            ++wid;
         }
-        t.unit = bu;
+        t.list = wl;
+        t.grp = wg;
         t.s0 = (int)(xi - bpu);
         t.s1 = (int)min((long long)min(n, t.s0 + 32 / a.pps), x1 - bpu);
         t.flags = (t.s0 == 0 || xi == x0 ? F_NEW : 0) | (t.s1 == n || bpu + t.s1 == x1 ? F_LAST : 0) |
@@ -362,25 +415,25 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (t.s0 == 0 && lane == 0) {
             // how many ranges the unit's first one shares it with
             const int r1 = (int)((bpu + n - 1) / per);
-            a.info[bu] = r1 == range ? make_int2(0, 0) : make_int2(range, r1 - range + 1);
+            a.info[wid] = r1 == range ? make_int4(0, 0, 0, 0) : make_int4(range, r1 - range + 1, wl, wg);
         }
         xi = bpu + t.s1;
         t.step = 1;
     };
     // steps 1 to 3, one dependent load each
     auto more = [&](Batch &t) {
-        const UnitAt w = unit_at(a, t.unit);
+        const ListAt w = list_at(a, t.list);
         if (t.step == 1) {
             const int c = t.s0 * a.pps + lane, e = c / a.sub;
             t.page = -1;
             t.gate = 0.f;
             t.nk = 0;
             if (lane < (t.s1 - t.s0) * a.pps && e < t.entries) {
-                const int n = paged_len(s, a.c.seq_len, w.b), local = (n + s.bs - 1) / s.bs - 1;
+                const int n = w.n, local = (n + s.bs - 1) / s.bs - 1;
                 int blk = e;
                 if (a.l.idx) {
-                    const int32_t *il = a.l.idx + w.lu * s.cap;
-                    const float *sc = a.l.score + w.lu * s.cap;
+                    const int32_t *il = a.l.idx + (size_t)t.list * s.cap;
+                    const float *sc = a.l.score + (size_t)t.list * s.cap;
                     const int before = e > 0 ? il[e - 1] : -1;
                     const float mine = sc[e], loc = sc[t.entries - 1];
                     blk = il[e];
@@ -418,7 +471,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // The batch being issued (its records are in shared memory) and the one
     // being loaded behind it, whose last step waits until it takes over.
     Batch nxt;
-    int cu_unit = -1, cu_s0 = 0, cu_n = 0, cu_flags = 0, ci = 0;   // unit, first stage, stages, flags, stages issued
+    // list, group, first stage, stages, flags, stages issued
+    int cu_list = -1, cu_grp = 0, cu_s0 = 0, cu_n = 0, cu_flags = 0, ci = 0;
     const uint32_t kb = smem_u32(sm) + warp * 2 * kHalfBytes, vb = kb + kHalfBytes;
     const uint32_t bar_k = smem_u32(&bars[warp][0]), bar_v = smem_u32(&bars[warp][1]);
     const uint32_t part_bytes = (uint32_t)a.rows * kD;
@@ -428,15 +482,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // scores, its values once that one has used its own, so one stage of
     // memory keeps one load in flight behind the arithmetic.
     uint32_t n_bytes = 0;
-    // flags, unit, first part (with the batch's half) and first key of that stage
-    int n_flags = 0, n_unit = 0, n_first = 0, n_key = 0;
+    // flags, list, group, first part (with the batch's half) and first key of that stage
+    int n_flags = 0, n_list = 0, n_grp = 0, n_first = 0, n_key = 0;
     auto issue_k = [&]() -> bool {              // false: the range is issued
         const bool fresh = ci == cu_n;
         if (fresh) {
-            if (nxt.unit < 0) return false;
+            if (nxt.list < 0) return false;
             ++batch;
             while (nxt.step < 4) more(nxt);
-            cu_unit = nxt.unit;
+            cu_list = nxt.list;
+            cu_grp = nxt.grp;
             cu_s0 = nxt.s0;
             cu_n = nxt.s1 - nxt.s0;
             cu_flags = nxt.flags;
@@ -447,7 +502,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const bool live = lane < a.pps && at.nk > 0;
         n_bytes = part_bytes * __popc(__ballot_sync(~0u, live));
         n_first = 32 * (batch & 1) + first;
-        n_unit = cu_unit;
+        n_list = cu_list;
+        n_grp = cu_grp;
         if (a.cu) {
             // every block in order: where the stage's keys lie, and whether
             // the unit's first row sees them all
@@ -480,7 +536,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const Place at = places[warp][min(31, ci * a.pps + lane)];
         if (lane < a.pps && at.nk > 0) tma_load_2d(vb + lane * part_bytes, &tmV, bar_v, 0, at.y);
         ++ci;
-        if (nxt.unit >= 0 && nxt.step < 3) more(nxt);
+        if (nxt.list >= 0 && nxt.step < 3) more(nxt);
     };
     open(nxt);
 
@@ -494,17 +550,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     bool ok = true, have = issue_k(), v_out = have, k_next = false;
     if (have) issue_v();
     for (; have; ++done) {
-        const int flags = n_flags, unit = n_unit, key0 = n_key;
+        const int flags = n_flags, list = n_list, grp = n_grp, key0 = n_key;
         const Part *part = &parts[warp][0][n_first];
         if (flags & F_NEW) {
             // the unit's queries: dimensions 16 k + 4 tq + {0, 1}, {2, 3} of head 8 n + gq
-            const UnitAt w = unit_at(a, unit);
+            const UnitAt w = unit_at(a, list, grp);
             acc.reset();
             if (a.cu) {
-                const int n = paged_len(s, a.c.seq_len, w.b);
-                lim0 = sees(a, w, n, 0);
+                lim0 = sees(a, w.l, w.r0);
 #pragma unroll
-                for (int i = 0; i < 2 * kNT; ++i) lim[i] = sees(a, w, n, 8 * (i >> 1) + 2 * tq + (i & 1));
+                for (int i = 0; i < 2 * kNT; ++i) lim[i] = sees(a, w.l, w.r0 + 8 * (i >> 1) + 2 * tq + (i & 1));
             }
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
@@ -752,7 +807,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 8);
                 acc.l[i] += __shfl_xor_sync(~0u, acc.l[i], 16);
             }
-            if (flags & F_WHOLE) acc.store(a, unit_at(a, unit), lane);
+            if (flags & F_WHOLE) acc.store(a, unit_at(a, list, grp), lane);
             else acc.save(a.rec + ((size_t)range * 2 + (flags & F_CUT ? 0 : 1)) * rec_floats<kD, kNT>(), lane);
         }
     }
@@ -780,7 +835,7 @@ paged_merge_kernel(DecArgs a) {
     const int u = blockIdx.x, lane = threadIdx.x & 31, slice = (threadIdx.x >> 5) % kSlices;
     const int grp = threadIdx.x / (32 * kSlices), i0 = slice * K;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int2 in = a.info[u];
+    const int4 in = a.info[u];
     if (in.y < 2) return;
     // the entry of the lane's rows that value k of the slice belongs to (a
     // slice is whole tiles of 4 kNT values, or at d = 64 a part of one)
@@ -865,7 +920,7 @@ paged_merge_kernel(DecArgs a) {
             for (int k = 0; k < K; ++k) o[k] = o[k] * pick(fa, k) + p[k][lane] * pick(fb, k);
         }
     }
-    const UnitAt w = unit_at(a, u);
+    const UnitAt w = unit_at(a, in.z, in.w);
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -903,14 +958,13 @@ long long rows_per_list(const PagedShape &s, bool chunk) {
     return chunk ? ((long long)s.tokens * s.G + s.B - 1) / s.B : s.heads_per;
 }
 int head_tiles(const PagedShape &s, bool chunk) { return rows_per_list(s, chunk) <= 8 ? 1 : 2; }
-// Groups of rows a list can have: with a chunk all its rows may be of one sequence.
-long long row_groups(const PagedShape &s, bool chunk) {
-    const int group = chunk ? 8 * head_tiles(s, true) : 16;
-    const long long most = chunk ? (long long)s.tokens * s.G : s.heads_per;
-    return (most + group - 1) / group;
-}
+int rows_per_group(const PagedShape &s, bool chunk) { return chunk ? 8 * head_tiles(s, true) : 16; }
+// The most units a call can have: a chunk's rows are shared out over the
+// sequences on the device.
 long long units_of(const PagedShape &s, bool chunk) {
-    return (long long)s.B * (chunk ? s.Hkv : s.Hsel) * row_groups(s, chunk);
+    const int group = rows_per_group(s, chunk);
+    return chunk ? ((long long)s.tokens * s.G / group + s.B) * s.Hkv
+                 : (long long)s.B * s.Hsel * ((s.heads_per + group - 1) / group);
 }
 size_t rec_bytes(const PagedShape &s, bool chunk) {
     return (size_t)(s.d / 16 * 4 + 4) * head_tiles(s, chunk) * 32 * sizeof(float);
@@ -943,14 +997,14 @@ bool paged_decode_supported(const PagedShape &s) {
 // A chunk of few rows reads the cache once per 16 of them here, at the decode's
 // rate; the tiles of paged_prefill.cu take 256 rows in about twice the time of
 // one pass, so up to some 40 rows a sequence are better off here (8 sequences
-// of 5000 keys with 20 rows per kv-head: ... us against 56).  The units of the
-// step line must stay few enough for every CTA to look through.
+// of 5000 keys with 20 rows per kv-head: 42 us against 56; 64 of 16K with 16
+// rows: 239 against 677).
 bool paged_rows_supported(const PagedShape &s) {
-    return s.dtype == SA_BF16 && s.tokens > 0 && rows_per_list(s, true) <= 40 && units_of(s, true) <= 16384;
+    return s.dtype == SA_BF16 && s.tokens > 0 && rows_per_list(s, true) <= 40 && (long long)s.tokens * s.G < (1ll << 30);
 }
 
 size_t paged_decode_scratch(const PagedShape &s, bool chunk) {
-    return ((units_of(s, chunk) * sizeof(int2) + 255) & ~(size_t)255) +
+    return ((units_of(s, chunk) * sizeof(int4) + 255) & ~(size_t)255) +
            (size_t)kMaxGrid * kMaxWarps * 2 * rec_bytes(s, chunk);
 }
 
@@ -974,11 +1028,11 @@ cudaError_t launch_paged_decode(const PagedShape &shape, const void *q, const in
     a.o = (__nv_bfloat16 *)o;
     a.lse = lse;
     a.status = status;
-    a.hg = (int)row_groups(s, chunk);
-    a.group = chunk ? 8 * head_tiles(s, true) : 16;
+    a.lists = s.B * s.Hsel;
+    a.group = rows_per_group(s, chunk);
     a.units = (int)units_of(s, chunk);
-    a.info = (int2 *)scratch;
-    a.rec = (float *)((unsigned char *)scratch + (((size_t)a.units * sizeof(int2) + 255) & ~(size_t)255));
+    a.info = (int4 *)scratch;
+    a.rec = (float *)((unsigned char *)scratch + (((size_t)a.units * sizeof(int4) + 255) & ~(size_t)255));
     // a page of up to 64 tokens is one part, a longer one two; small pages
     // share a stage (not in hierarchical mode, where a stage is one block)
     a.sub = s.bs > 64 ? 2 : 1;

@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(1024)
 paged_plan_kernel(PreArgs a) {
     extern __shared__ int off_s[];
     __shared__ long long tmp[32];
+    __shared__ int bad_s;
     const PagedShape &s = a.s;
     const int tid = threadIdx.x, tpu = 2 * a.tpt;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -175,16 +176,19 @@ paged_plan_kernel(PreArgs a) {
         }
         return;
     }
+    if (tid == 0) bad_s = 0;
+    __syncthreads();
     const int share = (s.B + 1023) / 1024, b0 = min(s.B, tid * share), b1 = min(s.B, b0 + share);
     long long n = 0, total;
     for (int b = b0; b < b1; ++b) {
         int r0, r1;
         rows_of(a, b, r0, r1);
         n += (r1 - r0 + tpu - 1) / tpu;
+        if (!(a.cu[b] >= 0 && a.cu[b] <= a.cu[b + 1] && a.cu[b + 1] <= s.tokens)) bad_s = 1;
     }
     long long at = scan1024(n, tmp, total) - n;
-    // offsets that overlap would list more units than rows
-    const bool bad = total > a.cap_tiles;
+    // offsets that do not ascend within the rows: nothing is done
+    const bool bad = bad_s;
     for (int b = b0; b < b1; ++b) {
         int r0, r1;
         rows_of(a, b, r0, r1);

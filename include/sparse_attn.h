@@ -528,7 +528,9 @@ int sparse_attn_paged_decode(const sa_paged_params *p, const void *q, const void
  * prompt, drafted tokens); without, it sees all seq_len[b] keys (cross
  * attention to states of another length).  Every block is read: SA_GATE and
  * SA_HIER are SA_ERR_UNSUPPORTED.  O [tokens, Hq, d], lse [tokens, Hq]; a row
- * that sees no key gives O = 0, lse = -inf; rows from cu[B] on are left. */
+ * that sees no key gives O = 0, lse = -inf; rows from cu[B] on are left.
+ * Offsets that do not ascend from 0 or more to at most `tokens` set status bit
+ * 1, and no row is written. */
 int sparse_attn_paged_prefill(const sa_paged_params *p, const void *Q, const int32_t *cu, const void *K8,
                               const void *V8, const float *kscale, const float *vscale, const int32_t *table,
                               const int32_t *seq_len, void *O, float *lse, void *ws, size_t ws_bytes, void *stream);

@@ -489,6 +489,26 @@ def run_chunks(causal, code, dtype, d, block, Hq, Hkv, grown):
                 check_row(dtype, O[cu[b] + t, h], lse[cu[b] + t, h], ref, see, d, (b, t, h))
 
 
+@pytest.mark.parametrize("tokens", [12, 400])
+def test_prefill_refuses_offsets_that_overlap(tokens):
+    p = sa.make_paged_params(4, 8, 2, 128, 64, 40, 8, tokens, flags=sa.SA_CAUSAL)
+    cache, _, _ = random_cache(p, 8)
+    lens = [400, 100, 64, 500]
+    table = i32(random_table(p, lens, 8).tolist())
+    q = torch.randn(tokens, 8, 128, device="cuda").bfloat16()
+    ws = sa.paged_workspace(p)
+    for cu in ([0, tokens, 0, tokens, 0], [0, 1, 2, 3, tokens + 1], [-1, 1, 2, 3, 4], [0, 3, 2, 3, 4]):
+        out = (torch.full_like(q, 5.0), torch.full((tokens, 8), 5.0, device="cuda"))
+        sa.paged_prefill(p, q, i32(cu), cache, table, i32(lens), ws, out=out)
+        torch.cuda.synchronize()
+        assert sa.sparse_attn_check_status(ws.data_ptr(), 0) == (sa.SA_ERR_DEVICE, 1)
+        assert (out[0] == 5).all() and (out[1] == 5).all()
+    cu = i32([0, tokens // 2, tokens // 2, tokens, tokens])
+    O, lse = sa.paged_prefill(p, q, cu, cache, table, i32(lens), ws)      # the next call is whole
+    done(ws)
+    assert torch.isfinite(O.float()).all() and torch.isfinite(lse).sum() > 0
+
+
 def test_prefill_rows_are_decodes():
     """One query per sequence: the chunk call and the decode call agree."""
     lens = [5000, 64, 1]
