@@ -665,17 +665,17 @@ def _paged_cache(what, p, cache):
     return dev
 
 
-def _paged_call(what, device, stream, fn, *args):
-    """fn(*args, stream) with `device` current, on its current stream unless
-    one is given; raises on an error code."""
+def _paged_call(what, device, stream, ws, fn, *args):
+    """fn(*args, workspace, its bytes, stream) with `device` current, on its
+    current stream unless one is given; raises on an error code."""
     torch = _torch()
-    if device < 0:
-        raise SparseAttnError(SA_ERR_ARG, f"{what}: tensors must be on a CUDA device")
+    if device < 0 or ws.get_device() != device or not ws.is_contiguous():
+        raise SparseAttnError(SA_ERR_ARG, f"{what}: tensors and a dense workspace must be on one CUDA device")
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _paged_call(what, device, stream, fn, *args)
+            return _paged_call(what, device, stream, ws, fn, *args)
     st = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    rc = fn(*args, st)
+    rc = fn(*args, ws.data_ptr(), ws.nbytes, st)
     if rc != SA_OK:
         raise SparseAttnError(rc, what)
 
@@ -705,9 +705,9 @@ def paged_tables(p: sa_paged_params, cur_len, new_len, free_pages, n_free, table
     _same("paged_tables", dev, ("cur_len", cur_len, i32, B), ("new_len", new_len, i32, B),
           ("free_pages", free_pages, i32, p.pages), ("n_free", n_free, i32, 1), ("table", table, i32, B * p.max_blocks),
           ("n_free_out", n_out, i32, 1), ("cu", cu, i32, B + 1), ("slot", slot, i64, tokens))
-    _paged_call("sparse_attn_paged_tables", dev, stream, (_lib or lib()).sparse_attn_paged_tables, p, cur_len.data_ptr(),
+    _paged_call("sparse_attn_paged_tables", dev, stream, ws, (_lib or lib()).sparse_attn_paged_tables, p, cur_len.data_ptr(),
                 new_len.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), n_out.data_ptr(), table.data_ptr(),
-                cu.data_ptr(), slot.data_ptr(), ws.data_ptr(), ws.numel())
+                cu.data_ptr(), slot.data_ptr())
     return out
 
 
@@ -724,9 +724,9 @@ def paged_append(p: sa_paged_params, K, V, slot, cache, ws, cu=None, new_len=Non
         _same("paged_append", dev, ("L", L, types[3] if p.dtype else types[2], p.B * p.Hkv * p.max_blocks * p.d),
               ("cu", cu, types[4], p.B + 1), ("new_len", new_len, types[4], p.B))
     K8, V8, ks, vs = cache
-    _paged_call("sparse_attn_paged_append", dev, stream, (_lib or lib()).sparse_attn_paged_append, p, K.data_ptr(), V.data_ptr(),
+    _paged_call("sparse_attn_paged_append", dev, stream, ws, (_lib or lib()).sparse_attn_paged_append, p, K.data_ptr(), V.data_ptr(),
                 ts, hs, slot.data_ptr(), _ptr(cu), _ptr(new_len), K8.data_ptr(), V8.data_ptr(), ks.data_ptr(),
-                vs.data_ptr(), _ptr(L), ws.data_ptr(), ws.numel())
+                vs.data_ptr(), _ptr(L))
     return cache
 
 
@@ -742,9 +742,8 @@ def paged_gather(p: sa_paged_params, slot, cache, ws, out=None, stream=None):
     K, V = out
     ts, hs = _row_strides("paged_gather", p, K, V, dev)
     _same("paged_gather", dev, ("slot", slot, types[5], p.tokens))
-    _paged_call("sparse_attn_paged_gather", dev, stream, (_lib or lib()).sparse_attn_paged_gather, p, slot.data_ptr(),
-                K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), K.data_ptr(), V.data_ptr(), ts, hs,
-                ws.data_ptr(), ws.numel())
+    _paged_call("sparse_attn_paged_gather", dev, stream, ws, (_lib or lib()).sparse_attn_paged_gather, p, slot.data_ptr(),
+                K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), K.data_ptr(), V.data_ptr(), ts, hs)
     return out
 
 
@@ -766,9 +765,9 @@ def paged_decode(p: sa_paged_params, q, cache, table, seq_len, ws, lists=None, o
         u = B * _hsel(p)
         m = u * (p.top_k + 2)
         _same("paged_decode", dev, ("idx", idx, i32, m), ("score", sc, f32, m), ("count", cnt, i32, u))
-    _paged_call("sparse_attn_paged_decode", dev, stream, (_lib or lib()).sparse_attn_paged_decode, p, q.data_ptr(),
+    _paged_call("sparse_attn_paged_decode", dev, stream, ws, (_lib or lib()).sparse_attn_paged_decode, p, q.data_ptr(),
                 K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(), seq_len.data_ptr(),
-                _ptr(idx), _ptr(sc), _ptr(cnt), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+                _ptr(idx), _ptr(sc), _ptr(cnt), o.data_ptr(), lse.data_ptr())
     return o, lse
 
 
@@ -782,9 +781,9 @@ def paged_prefill(p: sa_paged_params, Q, cu, cache, table, seq_len, ws, out=None
     O, lse = out if out is not None else (_torch().empty_like(Q), ks.new_empty((p.tokens, p.Hq)))
     _same("paged_prefill", dev, ("Q", Q, dt, n * p.d), ("O", O, dt, n * p.d), ("lse", lse, f32, n),
           ("cu", cu, i32, p.B + 1), ("table", table, i32, p.B * p.max_blocks), ("seq_len", seq_len, i32, p.B))
-    _paged_call("sparse_attn_paged_prefill", dev, stream, (_lib or lib()).sparse_attn_paged_prefill, p, Q.data_ptr(),
+    _paged_call("sparse_attn_paged_prefill", dev, stream, ws, (_lib or lib()).sparse_attn_paged_prefill, p, Q.data_ptr(),
                 cu.data_ptr(), K8.data_ptr(), V8.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(),
-                seq_len.data_ptr(), O.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+                seq_len.data_ptr(), O.data_ptr(), lse.data_ptr())
     return O, lse
 
 

@@ -132,7 +132,7 @@ paged_simt_kernel(SimtArgs a, const T *__restrict__ q, T *__restrict__ o, float 
 #pragma unroll
             for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
             if (mx > st.m) st.raise(mx);
-            const float p = st.m == -CUDART_INF_F ? 0.f : exp2f(z - st.m);
+            const float p = exp2f(z - (st.m == -CUDART_INF_F ? 0.f : st.m));
             float ps = p;
 #pragma unroll
             for (int w = 16; w; w >>= 1) ps += __shfl_xor_sync(~0u, ps, w);
@@ -173,7 +173,7 @@ paged_simt_kernel(SimtArgs a, const T *__restrict__ q, T *__restrict__ o, float 
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) x += f[w] == 0.f ? 0.f : sm_acc[w][i] * f[w];
-        from_f(o[((size_t)r * s.Hq + h) * kD + i], lt == 0.f ? 0.f : x * inv);
+        from_f(o[((size_t)r * s.Hq + h) * kD + i], lt == 0.f ? 0.f : lt == lt ? x * inv : lt);
     }
     if (tid == 0) lse[(size_t)r * s.Hq + h] = lt == 0.f ? -CUDART_INF_F : (M + log2f(lt)) * kLn2;
 }

@@ -806,7 +806,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             ++done;
             tc_fence_after();
-            const float inv = l == 0.f || mv_run == -CUDART_INF_F ? 0.f : ex2(mv_run - m_run) / l;
+            const float inv = l == 0.f ? 0.f : mv_run == -CUDART_INF_F ? 0.f * l : ex2(mv_run - m_run) / l;   // NaN stays NaN
             float *rec = a.rec + ((size_t)blockIdx.x * 2 + (g.out == 2 ? 1 : 0)) * (kD + 3) * 256 + 128 * q + r;
 #pragma unroll
             for (int cc = 0; cc < kD / 32; ++cc) {
@@ -873,12 +873,12 @@ paged_prefill_merge_kernel(PreArgs a) {
     for (int i = 0; i < job.n; ++i) {
         const float *p = rec(i);
         const float m = p[kD * 256], v = p[(kD + 2) * 256], f = v == -CUDART_INF_F ? 0.f : ex2(v - MV);
-        l += m == -CUDART_INF_F ? 0.f : p[(kD + 1) * 256] * ex2(m - M);
+        l += p[(kD + 1) * 256] * (m == -CUDART_INF_F ? 1.f : ex2(m - M));     // at -inf it is 0, or NaN
 #pragma unroll
         for (int k = 0; k < NC; ++k) o[k] += p[(warp * NC + k) * 256] * f;
     }
     const size_t row = (size_t)(job.row0 + tok) * a.s.Hq + job.h * a.s.G + head;
-    const float inv = l == 0.f || MV == -CUDART_INF_F ? 0.f : ex2(MV - M) / l;
+    const float inv = l == 0.f ? 0.f : MV == -CUDART_INF_F ? 0.f * l : ex2(MV - M) / l;
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = l == 0.f ? 0.f : o[k] * inv;
 #pragma unroll

@@ -111,6 +111,20 @@ def test_tables_follow_the_oracle(B, block, maxb, steps):
         n_free, table, free, cur = int(n[0]), t, f, want
 
 
+def test_tables_of_the_most_sequences():
+    B, block, maxb = 16384, 16, 4
+    rng = np.random.default_rng(0)
+    want = [int(x) for x in rng.integers(0, maxb * block + 1, B)]
+    pages = B * maxb
+    free = list(rng.permutation(pages))
+    table = np.full((B, maxb), -1, np.int32)
+    p = sa.make_paged_params(B, 1, 1, 64, block, pages, maxb, sum(want))
+    ref = op.tables([0] * B, want, free, pages, table, block, sum(want))
+    ws, t, f, (n, cu, slot) = run_tables(p, [0] * B, want, free, pages, table)
+    assert sa.check_status(ws) == 0
+    assert n[0] == ref[0] and list(cu) == ref[3] and list(slot) == ref[4] and np.array_equal(t, ref[1])
+
+
 @pytest.mark.parametrize("cur,want,n_free,tokens,bits", [
     ([0, 5], [40, 5], 2, 64, 16),           # three pages wanted, two free
     ([0, 5], [30, 5], 2, 29, 16),           # thirty slots wanted
@@ -632,3 +646,100 @@ def test_a_call_runs_on_the_stream_it_is_given():
     got = sa.paged_decode(p, q, cache, table, n, ws, stream=side)
     side.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(ref, got))
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_a_cache_beyond_32_bit_offsets(code):
+    """Codes of more than 4 GiB: the last pages are appended to, read back and
+    attended to like the first ones."""
+    block, H, d = 64, 2, 128
+    pages = 4 * (1 << 30) // (block * H * d) + 300
+    p = sa.make_paged_params(1, 8, H, d, block, pages, 16, 900, flags=sa.SA_CAUSAL, code=code)
+    small = sa.make_paged_params(1, 8, H, d, block, 16, 16, 900, flags=sa.SA_CAUSAL, code=code)
+    ct = torch.float8_e4m3fn if code == "e4m3" else torch.int8
+    shape = (pages, H, block, d)
+    big = tuple(torch.empty(shape, dtype=torch.uint8, device="cuda").view(ct) for _ in "kv") + tuple(
+        torch.zeros(shape[:2], device="cuda") for _ in "kv")
+    ref = sa.paged_cache(small)
+    tables = [torch.arange(pages - 16, pages, device="cuda").int(), torch.arange(16, device="cuda").int()]
+    K, V = (torch.randn(900, H, d, device="cuda").bfloat16() for _ in "kv")
+    Q = torch.randn(900, 8, d, device="cuda").bfloat16()
+    pos, cu, n = torch.arange(900, device="cuda"), i32([0, 900]), i32([900])
+    got = []
+    for q, cache, table in ((p, big, tables[0]), (small, ref, tables[1])):
+        ws = sa.paged_workspace(q)
+        slot = table.long()[pos // block] * block + pos % block
+        sa.paged_append(q, K, V, slot, cache, ws)
+        back = sa.paged_gather(q, slot, cache, ws)
+        O, lse = sa.paged_prefill(q, Q, cu, cache, table, n, ws)
+        one = sa.make_paged_params(1, 8, H, d, block, q.pages, 16, 3, flags=sa.SA_CAUSAL, code=code)
+        o3, lse3 = sa.paged_prefill(one, Q[:3].contiguous(), i32([0, 3]), cache, table, n, ws)
+        o, l1 = sa.paged_decode(q, Q[:1].contiguous(), cache, table, n, ws)
+        done(ws)
+        got.append((*back, O, lse, o3, lse3, o, l1))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("tokens,grown", [(24, [9, 3]), (600, [333, 120])])
+def test_prefill_captured_and_replayed(tokens, grown):
+    p = sa.make_paged_params(2, 8, 2, 128, 64, 40, 16, tokens, flags=sa.SA_CAUSAL)
+    cache, _, _ = random_cache(p, 2)
+    lens = [700, 450]
+    table, n, cu = i32(random_table(p, [1000, 1000], 2).tolist()), i32(lens), i32([0, grown[0], sum(grown)])
+    Q = torch.randn(tokens, 8, 128, device="cuda").bfloat16()
+    ws = sa.paged_workspace(p)
+    sa.paged_prefill(p, Q, cu, cache, table, n, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        O, lse = sa.paged_prefill(p, Q, cu, cache, table, n, ws)
+    for step in range(3):
+        n.copy_(i32([700 + 97 * step, 450 - 64 * step]))
+        cu.copy_(i32([0, grown[0] - step, sum(grown) - 2 * step]))
+        Q.normal_()
+        O.fill_(5)
+        g.replay()
+        ref, rl = sa.paged_prefill(p, Q, cu, cache, table, n, sa.paged_workspace(p))
+        done(ws)
+        m = sum(grown) - 2 * step
+        assert torch.equal(O[:m], ref[:m]) and torch.equal(lse[:m], rl[:m]) and (O[m:] == 5).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    p = sa.make_paged_params(4, 8, 2, 128, 64, 200, 40, 300, flags=sa.SA_CAUSAL)
+    cache, _, _ = random_cache(p, 2)
+    lens = [2500, 77, 1, 1300]
+    table, n, cu = i32(random_table(p, lens, 2).tolist()), i32(lens), i32([0, 200, 201, 202, 300])
+    q, Q = torch.randn(4, 8, 128, device="cuda").bfloat16(), torch.randn(300, 8, 128, device="cuda").bfloat16()
+    ref = (*sa.paged_decode(p, q, cache, table, n, sa.paged_workspace(p)),
+           *sa.paged_prefill(p, Q, cu, cache, table, n, sa.paged_workspace(p)))
+    ws, streams = [sa.paged_workspace(p) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(streams[0]):
+            a = sa.paged_decode(p, q, cache, table, n, ws[0])
+        with torch.cuda.stream(streams[1]):
+            b = sa.paged_prefill(p, Q, cu, cache, table, n, ws[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ref, (*a, *b)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_query_that_is_not_a_number_spoils_its_own_row(dtype):
+    p = sa.make_paged_params(3, 8, 2, 128, 64, 40, 16, 300, flags=sa.SA_CAUSAL, dtype=dtype)
+    cache, _, _ = random_cache(p, 2)
+    table, n, cu = i32(random_table(p, [500] * 3, 2).tolist()), i32([500, 321, 64]), i32([0, 150, 299, 300])
+    Q = torch.randn(300, 8, 128, device="cuda").to(T[dtype])
+    ws = sa.paged_workspace(p)
+    O, lse = sa.paged_prefill(p, Q, cu, cache, table, n, ws)
+    o, l1 = sa.paged_decode(p, Q[:3].contiguous(), cache, table, n, ws)
+    bad = Q.clone()
+    bad[1, 3, 7], bad[200, 0, 0] = math.nan, math.inf
+    O2, lse2 = sa.paged_prefill(p, bad, cu, cache, table, n, ws)
+    o2, l2 = sa.paged_decode(p, bad[:3].contiguous(), cache, table, n, ws)
+    done(ws)
+    keep = torch.ones(300, 8, dtype=torch.bool, device="cuda")
+    keep[1, 3] = keep[200, 0] = False
+    assert torch.equal(O[keep], O2[keep]) and torch.equal(lse[keep], lse2[keep]) and torch.isnan(O2[1, 3].float()).all()
+    assert torch.equal(o[keep[:3]], o2[keep[:3]]) and torch.equal(l1[keep[:3]], l2[keep[:3]]) and torch.isnan(o2[1, 3].float()).all()

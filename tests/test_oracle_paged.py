@@ -181,6 +181,8 @@ def test_the_binding_refuses_other_tensors():
         lambda: sa.paged_decode(p, q, cache, table.long(), n, ws),
         lambda: sa.paged_prefill(p, q, n, cache, table, n, ws),
         lambda: sa.paged_tables(p, n, n, n, n, table, ws),
+        lambda: sa.paged_gather(p, slot, cache, ws),                   # all in order, but not on a GPU
+        lambda: sa.paged_decode(p, q, cache, table, n, ws),
     ):
         with pytest.raises(sa.SparseAttnError) as e:
             call()
