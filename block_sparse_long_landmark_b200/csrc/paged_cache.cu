@@ -228,16 +228,28 @@ template <> struct Sum8<SA_E4M3> {
     __device__ __forceinline__ float get(int e) const { return v[e]; }
 };
 template <> struct Sum8<SA_INT8> {
-    int v[8];
+    unsigned v[4];
+    int n;
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0;
+        for (int e = 0; e < 4; ++e) v[e] = 0;
+        n = 0;
     }
+    // bytes 0, 2 and 1, 3 of a word in 16 bits each, 128 too large every time
+    // (at most 128 rows of 255)
     __device__ __forceinline__ void add(uint2 c) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += (int)((e < 4 ? c.x : c.y) << (24 - 8 * (e & 3))) >> 24;
+        c.x ^= 0x80808080u;
+        c.y ^= 0x80808080u;
+        v[0] += c.x & 0x00ff00ffu;
+        v[1] += (c.x >> 8) & 0x00ff00ffu;
+        v[2] += c.y & 0x00ff00ffu;
+        v[3] += (c.y >> 8) & 0x00ff00ffu;
+        ++n;
     }
-    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+    __device__ __forceinline__ float get(int e) const {
+        const unsigned w = v[(e >> 2) * 2 + (e & 1)];
+        return (float)((int)(e & 2 ? w >> 16 : w & 0xffffu) - 128 * n);
+    }
 };
 
 // Eight finite values with |y inv| <= M to codes, inv a power of two.
