@@ -691,7 +691,10 @@ def _row_strides(what, p, K, V, device):
             raise SparseAttnError(SA_ERR_ARG, f"{what}: {name} must be {dt} {shape} on device {device} with the strides "
                                               "of the other and a dense last dimension")
     hs = st[1] if shape[1] > 1 else shape[2]
-    return (st[0] if shape[0] > 1 else shape[1] * hs), hs
+    ts = st[0] if shape[0] > 1 else shape[1] * hs
+    if p.tokens and (ts < p.d or hs < p.d):      # 0, 0 would mean dense rows to the library
+        raise SparseAttnError(SA_ERR_ARG, f"{what}: expanded rows (strides {st}) are not taken")
+    return ts, hs
 
 
 def paged_tables(p: sa_paged_params, cur_len, new_len, free_pages, n_free, table, ws, out=None, stream=None):

@@ -187,3 +187,15 @@ def test_the_binding_refuses_other_tensors():
         with pytest.raises(sa.SparseAttnError) as e:
             call()
         assert e.value.code == sa.SA_ERR_ARG
+
+
+def test_the_binding_refuses_expanded_rows():
+    """Strides of 0 and 0 mean dense rows to the library: never an expanded tensor's."""
+    p, one = _p(tokens=4, Hkv=2), _p(tokens=1, Hkv=2)
+    ws, x = torch.zeros(1 << 16, dtype=torch.uint8), torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    for q in (p, one):
+        cache, slot, rows = sa.paged_cache(q, device="cpu"), torch.zeros(q.tokens, dtype=torch.int64), x.expand(q.tokens, 2, 128)
+        for call in (lambda: sa.paged_append(q, rows, rows, slot, cache, ws),
+                     lambda: sa.paged_gather(q, slot, cache, ws, out=(rows, rows))):
+            with pytest.raises(sa.SparseAttnError, match="expanded"):
+                call()
