@@ -67,7 +67,15 @@ paged_simt_kernel(SimtArgs a, const T *__restrict__ q, T *__restrict__ o, float 
     const int r = blockIdx.x, h = blockIdx.y, g = h / s.G;
     int b = r, keys;
     if (a.cu) {
-        if (r >= a.cu[s.B] || r < 0) return;      // rows behind the last sequence stay as they are
+        // offsets that do not ascend within the rows: nothing is done
+        int bad = 0;
+        for (int i = tid; i < s.B; i += 128)
+            bad |= !(a.cu[i] >= 0 && a.cu[i] <= a.cu[i + 1] && a.cu[i + 1] <= s.tokens);
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) set_status(a.status, kStatusBadIndex);
+            return;
+        }
+        if (r < a.cu[0] || r >= a.cu[s.B]) return;      // rows of no sequence stay as they are
         b = row_owner(a.cu, s.B, r);
         const int n = paged_len(s, a.c.seq_len, b);
         keys = s.flags & SA_CAUSAL ? max(0, n - (a.cu[b + 1] - r) + 1) : n;

@@ -503,13 +503,13 @@ def run_chunks(causal, code, dtype, d, block, Hq, Hkv, grown):
                 check_row(dtype, O[cu[b] + t, h], lse[cu[b] + t, h], ref, see, d, (b, t, h))
 
 
-@pytest.mark.parametrize("tokens", [12, 400])
-def test_prefill_refuses_offsets_that_overlap(tokens):
-    p = sa.make_paged_params(4, 8, 2, 128, 64, 40, 8, tokens, flags=sa.SA_CAUSAL)
+@pytest.mark.parametrize("tokens,dtype", [(12, "bf16"), (400, "bf16"), (12, "fp32")])
+def test_prefill_refuses_offsets_that_overlap(tokens, dtype):
+    p = sa.make_paged_params(4, 8, 2, 128, 64, 40, 8, tokens, flags=sa.SA_CAUSAL, dtype=dtype)
     cache, _, _ = random_cache(p, 8)
     lens = [400, 100, 64, 500]
     table = i32(random_table(p, lens, 8).tolist())
-    q = torch.randn(tokens, 8, 128, device="cuda").bfloat16()
+    q = torch.randn(tokens, 8, 128, device="cuda").to(T[dtype])
     ws = sa.paged_workspace(p)
     for cu in ([0, tokens, 0, tokens, 0], [0, 1, 2, 3, tokens + 1], [-1, 1, 2, 3, 4], [0, 3, 2, 3, 4]):
         out = (torch.full_like(q, 5.0), torch.full((tokens, 8), 5.0, device="cuda"))
@@ -521,6 +521,20 @@ def test_prefill_refuses_offsets_that_overlap(tokens):
     O, lse = sa.paged_prefill(p, q, cu, cache, table, i32(lens), ws)      # the next call is whole
     done(ws)
     assert torch.isfinite(O.float()).all() and torch.isfinite(lse).sum() > 0
+
+
+@pytest.mark.parametrize("tokens,dtype", [(12, "bf16"), (400, "bf16"), (12, "fp32")])
+def test_prefill_leaves_rows_before_the_first_sequence(tokens, dtype):
+    p = sa.make_paged_params(2, 4, 1, 64, 32, 40, 8, tokens, flags=sa.SA_CAUSAL, dtype=dtype)
+    cache, _, _ = random_cache(p, 8)
+    table, lens, ws = i32(random_table(p, [250, 250], 8).tolist()), i32([250, 250]), sa.paged_workspace(p)
+    q = torch.randn(tokens, 4, 64, device="cuda").to(T[dtype])
+    out = (torch.full_like(q, 5.0), torch.full((tokens, 4), 5.0, device="cuda"))
+    sa.paged_prefill(p, q, i32([3, 5, tokens - 2]), cache, table, lens, ws, out=out)
+    done(ws)
+    rows = torch.tensor([False] * 3 + [True] * (tokens - 5) + [False] * 2)
+    for x in out:
+        assert ((x.cpu() == 5).flatten(1).all(1) == ~rows).all()
 
 
 def test_prefill_rows_are_decodes():
