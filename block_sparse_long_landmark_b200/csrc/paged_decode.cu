@@ -9,11 +9,15 @@
 //   * the work is one line of stages (up to 64 keys of one unit: a page, half
 //     a page of more than 64 tokens, or several small pages), units one after
 //     the other, cut into equal ranges, one per warp of the grid whatever the
-//     lengths or lists are.  A warp streams its range by itself: it issues the
-//     TMA loads of its own ring, waits for them and computes; no warp waits
-//     for another.  A unit that lies in one range is finished by its warp; the
-//     others leave a record (max, sum, acc) per range, at most two a warp,
-//     which a second launch joins in range order;
+//     lengths or lists are.  A warp streams its range by itself, through one
+//     stage of shared memory: the next stage's keys are sent for once this
+//     one's scores are made, its values once this one's are used; no warp
+//     waits for another (twelve warps with a stage each keep more in flight
+//     than six with two).  A unit that lies in one range is finished by its
+//     warp; the others leave a record (max, sum, acc) per range, at most two a
+//     warp, which a second launch joins in range order;
+//   * a unit is a list's query heads, up to 16; a chunk of few rows (drafted
+//     tokens) is units of 8 or 16 rows, each with its keys per row;
 //   * codes become fp16 in registers (exact), so the tensor core multiplies
 //     them as they are, and scales stay out of the matrices: a key's scale
 //     multiplies its logits, a value's the finished product of its page;
@@ -63,6 +67,7 @@ struct DecArgs {
     float *rec;          // [ranges][2] records
     const int32_t *cu;   // packed chunk rows, or null: one query per sequence
     int lists, units;    // B * Hsel lists; the most units (groups of a list's rows) there can be
+    int ranges;          // warps of the grid
     int group;           // rows per group
     int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
 };
@@ -364,8 +369,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             a.info[id] = make_int4(0, 0, 0, 0);
     }
     const long long total = pre[kThreads];
-    const int ranges = gridDim.x * kWarps;
-    const long long per = max((long long)kMinRange, (total + ranges - 1) / ranges);
+    const long long per = max((long long)kMinRange, (total + a.ranges - 1) / a.ranges);
     // neighbouring ranges go to different SMs, so that a small call spreads out
     const int range = warp * gridDim.x + blockIdx.x;
     const long long x0 = range * per, x1 = min(total, x0 + per);
@@ -470,7 +474,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     };
     // The batch being issued (its records are in shared memory) and the one
     // being loaded behind it, whose last step waits until it takes over.
-    Batch nxt;
+    Batch nxt{};
     // list, group, first stage, stages, flags, stages issued
     int cu_list = -1, cu_grp = 0, cu_s0 = 0, cu_n = 0, cu_flags = 0, ci = 0;
     const uint32_t kb = smem_u32(sm) + warp * 2 * kHalfBytes, vb = kb + kHalfBytes;
@@ -836,7 +840,10 @@ paged_merge_kernel(DecArgs a) {
     const int grp = threadIdx.x / (32 * kSlices), i0 = slice * K;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 in = a.info[u];
-    if (in.y < 2) return;
+    // a range whose wait ran out may have left the entry of another call
+    if (in.y < 2 || in.x < 0 || in.y > a.ranges - in.x || in.z < 0 || in.z >= a.lists || in.w < 0 ||
+        in.w >= a.units)
+        return;
     // the entry of the lane's rows that value k of the slice belongs to (a
     // slice is whole tiles of 4 kNT values, or at d = 64 a part of one)
     auto pick = [&](const float *f, int k) {
@@ -973,7 +980,8 @@ size_t rec_bytes(const PagedShape &s, bool chunk) {
 constexpr int kMaxGrid = 148;
 
 template <int kD, int kCode, int kNT>
-cudaError_t run(const DecArgs &a, int grid, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+cudaError_t run(DecArgs a, int grid, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+    a.ranges = grid * warps_of<kNT>();
     constexpr int smem = warps_of<kNT>() * 2 * 64 * kD + 1024;
     auto kern = a.pps == 1 ? paged_decode_kernel<kD, kCode, kNT, true> : paged_decode_kernel<kD, kCode, kNT, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
