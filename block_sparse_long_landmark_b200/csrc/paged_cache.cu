@@ -297,14 +297,15 @@ __device__ __forceinline__ int warp_owner(const int *off, int n, int x) {
 }
 
 // A run: consecutive slots of one page.  The CTA of (window, head, keys or
-// values) takes the runs that begin in its window.  A run's new rows, and for the landmark the codes
-// already in the block, are read into registers once: their largest magnitude
-// decides the scale (kept when the rows fit, else the power of two that holds
-// them, and the codes already there are rounded anew; scales are powers of
-// two, so a scaled value is exact and a code is one rounding of it), then the
-// codes are written and the block's cached keys meant into its landmark.
-// HBM bound for prompts (two bytes in, one out per value); a step of single
-// tokens is bound by its chain of reads: slot, rows, scale.
+// values) takes the runs that begin in its window.  A run's new rows, and for
+// the landmark the codes already in the block, are read into registers once:
+// their largest magnitude decides the scale (kept when the rows fit, else the
+// power of two that holds them, and the codes already there are rounded anew;
+// scales are powers of two, so a scaled value is exact and a code is one
+// rounding of it), then the codes are written and the mean of the block's
+// cached keys becomes its landmark.  A prompt's 30.6K tokens of 8 heads, int8:
+// 54 us, 29 at the copy rate (two bytes in, one out per value); bound by issue
+// slots (73 % used by eight CTAs an SM).
 template <typename T, int kCode, int kD, int kRows>
 __global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? (kRows == 64 ? 8 : 5) : kRows == 64 ? 4 : 2)
 paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__ V, long long ts, long long hs,
@@ -352,8 +353,10 @@ paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__
     uint8_t *codes = half ? V8 : K8;
     float *scales = half ? vs : ks;
     const bool mean = !half && L;
-    for (int w = 0; w < kWinMax / 32; ++w)
-    for (unsigned left = lead[w]; left; left &= left - 1) {
+    unsigned left = lead[0];
+    for (int w = 0;; left &= left - 1) {
+        while (!left && ++w < kWinMax / 32) left = lead[w];
+        if (!left) break;
         const int j = 32 * w + __ffs(left) - 1, first = sl[j + 1];
         int end = j + 1;                  // next break (a set bit always follows: bits from span on are set)
         while (!((brk[end >> 5] >> (end & 31)) & 1u)) {

@@ -35,6 +35,10 @@
 // both would hold one tile's products back while it waits, quarter by quarter,
 // for the other's weights: 3.39 against 3.06 ms for a 4K chunk at 32K), 2
 // loads codes and scales; 4-7 convert; 8-11 and 12-15 softmax.
+// The warps' loops share the instruction caches, so code is kept short: with
+// the issuers', converters', rescaling and epilogue loops unrolled, 114 KB, a 4K
+// chunk at 32K took 2.32 ms and any line more or less moved it by 10 %; rolled,
+// 78 KB, 2.11 ms, and it holds still.
 // Registers: launched at 128; 112 + 112 + 2 * 144 = 4 * 128.
 // Every wait is bounded; when one runs out the CTA sets the status word, lets
 // its copies land, frees tensor memory and exits.
@@ -298,7 +302,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + bar_off<kD>() + 8 * NBAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + bar_off<kD>() + 8 * NBAR + 4);
     Seg *segs = reinterpret_cast<Seg *>(smem + bar_off<kD>() + 512);                       // [2]
-    // [4][8]: per 16 keys the key scale, the value scale and its log2
+    // [4][8]: per 16 keys the key scale, the value scale, its log2, and 0 or,
+    // where the keys have no page, -inf for their logits
     float4 *scales = reinterpret_cast<float4 *>(smem + bar_off<kD>() + 640);
     static_assert(8 * NBAR + 8 <= 512 && 2 * sizeof(Seg) <= 128 && 640 + kScaleSlots * 128 <= 2048, "shared memory");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -421,7 +426,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         // S of half h of key tile gg (64 keys)
         auto qk = [&](int gg, int h) {
             const uint64_t db = desc_k_sw128(sbase + k_off<kD>() + (gg % kStages) * kTile + h * 8192);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < kD / 16; ++k) {
                 const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
                 mma_ss_w(tS + 64 * h, dq + off, db + off, idq, k > 0);
@@ -466,12 +471,14 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!(ok = wait(C_Q, n & 1))) break;
             if (!(ok = wait(C_KF + gt % kStages, (gt / kStages) & 1))) break;
             tc_fence_after();
-            qk(gt, 0);
-            qk(gt, 1);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) qk(gt, h);
             if (T == 1) mma_commit_w(bar(C_QFREE));
             for (int t = 0; ok && t < T; ++t, ++gt, ++gq) {
                 if (!(ok = wait(C_VF + gt % kStages, (gt / kStages) & 1))) break;
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
                     for (int e = 0; e < 2; ++e) {
                         if (!(ok = wait(C_P + 4 * q + 2 * h + e, gq & 1))) break;
                         tc_fence_after();
@@ -498,79 +505,93 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         mbar_wait_lazy(bar(C_END + q), 0, &never, a.status);
     } else if (warp == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        {
-            // ---- codes and scales of each key tile ----------------------------
-            const int boxes = 128 / a.box;
-            bool ok = true;
-            int gt = 0, klast = -1, vlast = -1;
-            for (int n = 0; ok; ++n) {
-                const int slot = n & 1;
-                ok = mbar_wait_lazy(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
-                if (!__all_sync(~0u, ok)) break;
-                const Seg g = segs[slot];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C_LF + slot));
-                if (g.tb == g.ta) break;
-                // lane i < 8: page of keys 128 t + 16 i .. + 15 (-1: none), its scales
-                auto page_at = [&](int t) {
-                    const int key = 128 * t + 16 * lane;
-                    return lane < 8 && t < g.tb && key < g.n ? a.c.table[(size_t)g.b * s.maxb + key / s.bs] : -1;
-                };
-                auto scale_at = [&](int &pg, float2 &f) {
-                    f = make_float2(0.f, 0.f);
-                    if (pg < 0 || pg >= s.pages) {
-                        if (pg != -1) set_status(a.status, kStatusBadIndex);
-                        pg = -1;
-                        return;
+        // ---- codes and scales of each key tile ----------------------------
+        const int boxes = 128 / a.box;
+        bool ok = true;
+        int gt = 0, klast = -1, vlast = -1;
+        for (int n = 0; ok; ++n) {
+            const int slot = n & 1;
+            ok = mbar_wait_lazy(bar(C_L + slot), (n >> 1) & 1, abort_flag, a.status);
+            if (!__all_sync(~0u, ok)) break;
+            const Seg g = segs[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C_LF + slot));
+            if (g.tb == g.ta) break;
+            // lane i < 8: page of keys 128 t + 16 i .. + 15 (-1: no such keys,
+            // -2: a table entry out of range), its scales
+            auto page_at = [&](int t) {
+                const int key = 128 * t + 16 * lane;
+                if (lane >= 8 || t >= g.tb || key >= g.n) return -1;
+                const int pg = a.c.table[(size_t)g.b * s.maxb + key / s.bs];
+                return pg < 0 ? -2 : pg;
+            };
+            auto scale_at = [&](int &pg, float2 &f) {
+                f = make_float2(0.f, 0.f);
+                if (pg < 0 || pg >= s.pages) {
+                    if (pg != -1) {
+                        set_status(a.status, kStatusBadIndex);
+                        pg = -2;
                     }
-                    const size_t ph = (size_t)pg * s.Hkv + g.h;
-                    f = make_float2(a.c.ks[ph], a.c.vs[ph]);
-                };
-                int pg = page_at(g.ta), pg1 = page_at(g.ta + 1);
-                float2 f, f1;
-                scale_at(pg, f);
-                for (int t = g.ta; t < g.tb; ++t, ++gt) {
-                    const int pg2 = page_at(t + 2);
-                    scale_at(pg1, f1);
-                    const int key = 128 * t + a.box * lane;
-                    const int mine = __shfl_sync(~0u, pg, (lane * a.box >> 4) & 7);
-                    const bool live = lane < boxes && mine >= 0 && key < g.n;
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(~0u, live)) * a.box * kD;
-                    const int y = (mine * s.Hkv + g.h) * s.bs + key % s.bs;
-                    const uint32_t dst = sbase + raw_off<kD>() + lane * a.box * kD;
-                    if (gt >= 1) ok = mbar_wait_lazy(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
-                    if (!__all_sync(~0u, ok)) { ok = false; break; }
-                    if (lane < 8)
-                        scales[(gt % kScaleSlots) * 8 + lane] = make_float4(f.x, f.y, log2f(f.y), 0.f);
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(C_SC + gt % kScaleSlots));
-                        if (bytes) mbar_expect_tx(bar(C_RK), bytes);
-                        else mbar_arrive(bar(C_RK));
-                    }
-                    __syncwarp();
-                    if (live) tma_load_2d(dst, &tmK, bar(C_RK), 0, y);
-                    klast = gt;
-                    if (gt >= 1) ok = mbar_wait_lazy(bar(C_RVF), (gt - 1) & 1, abort_flag, a.status);
-                    if (!__all_sync(~0u, ok)) { ok = false; break; }
-                    if (lane == 0) {
-                        if (bytes) mbar_expect_tx(bar(C_RV), bytes);
-                        else mbar_arrive(bar(C_RV));
-                    }
-                    __syncwarp();
-                    if (live) tma_load_2d(dst + 128 * kD, &tmV, bar(C_RV), 0, y);
-                    vlast = gt;
-                    pg = pg1;
-                    f = f1;
-                    pg1 = pg2;
+                    return;
                 }
+                const size_t ph = (size_t)pg * s.Hkv + g.h;
+                f = make_float2(a.c.ks[ph], a.c.vs[ph]);
+            };
+            // codes of keys without a page: zeros, so that nothing spoils the
+            // products with their weight of 0
+            auto zero = [&](uint32_t at) {
+                for (int i = 0; i < a.box * kD; i += 16)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + i), "r"(0) : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            };
+            int pg = page_at(g.ta), pg1 = page_at(g.ta + 1);
+            float2 f, f1;
+            scale_at(pg, f);
+            for (int t = g.ta; t < g.tb; ++t, ++gt) {
+                const int pg2 = page_at(t + 2);
+                scale_at(pg1, f1);
+                const int key = 128 * t + a.box * lane;
+                const int mine = __shfl_sync(~0u, pg, (lane * a.box >> 4) & 7);
+                const bool live = lane < boxes && mine >= 0 && key < g.n;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(~0u, live)) * a.box * kD;
+                const int y = (mine * s.Hkv + g.h) * s.bs + key % s.bs;
+                const uint32_t dst = sbase + raw_off<kD>() + lane * a.box * kD;
+                if (gt >= 1) ok = mbar_wait_lazy(bar(C_RKF), (gt - 1) & 1, abort_flag, a.status);
+                if (!__all_sync(~0u, ok)) { ok = false; break; }
+                if (lane < 8)
+                    scales[(gt % kScaleSlots) * 8 + lane] =
+                        make_float4(f.x, f.y, log2f(f.y), pg == -2 ? -CUDART_INF_F : 0.f);
+                if (lane < boxes && mine == -2) zero(dst);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C_SC + gt % kScaleSlots));
+                    if (bytes) mbar_expect_tx(bar(C_RK), bytes);
+                    else mbar_arrive(bar(C_RK));
+                }
+                __syncwarp();
+                if (live) tma_load_2d(dst, &tmK, bar(C_RK), 0, y);
+                klast = gt;
+                if (gt >= 1) ok = mbar_wait_lazy(bar(C_RVF), (gt - 1) & 1, abort_flag, a.status);
+                if (!__all_sync(~0u, ok)) { ok = false; break; }
+                if (lane < boxes && mine == -2) zero(dst + 128 * kD);
+                __syncwarp();
+                if (lane == 0) {
+                    if (bytes) mbar_expect_tx(bar(C_RV), bytes);
+                    else mbar_arrive(bar(C_RV));
+                }
+                __syncwarp();
+                if (live) tma_load_2d(dst + 128 * kD, &tmV, bar(C_RV), 0, y);
+                vlast = gt;
+                pg = pg1;
+                f = f1;
+                pg1 = pg2;
             }
-            if (lane == 0 && *abort_flag) {
-                // let the copies in flight land before the CTA exits (bounded)
-                volatile int never = 0;
-                if (klast >= 0) mbar_wait_lazy(bar(C_RK), klast & 1, &never, a.status);
-                if (vlast >= 0) mbar_wait_lazy(bar(C_RV), vlast & 1, &never, a.status);
-            }
+        }
+        if (lane == 0 && *abort_flag) {
+            // let the copies in flight land before the CTA exits (bounded)
+            volatile int never = 0;
+            if (klast >= 0) mbar_wait_lazy(bar(C_RK), klast & 1, &never, a.status);
+            if (vlast >= 0) mbar_wait_lazy(bar(C_RV), vlast & 1, &never, a.status);
         }
     } else if (warp < 8) {
         // ---- converters: codes -> fp16 tiles -----------------------------------
@@ -635,14 +656,16 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (ta == tb) break;
             for (int t = ta; t < tb; ++t, ++gt) {
                 const int st = gt % kStages, use = gt / kStages;
-                if (gt >= kStages && !(ok = wait(C_KE + st, (use - 1) & 1))) break;
-                if (!(ok = wait(C_RK, gt & 1))) break;
-                convert(raw, sbase + k_off<kD>() + st * kTile, false, C_RKF);
-                if (lane == 0) mbar_arrive(bar(C_KF + st));
-                if (gt >= kStages && !(ok = wait(C_VE + st, (use - 1) & 1))) break;
-                if (!(ok = wait(C_RV, gt & 1))) break;
-                convert(raw + 128 * kD, sbase + v_off<kD>() + st * kTile, 128 * (t + 1) > keys, C_RVF);
-                if (lane == 0) mbar_arrive(bar(C_VF + st));
+                // keys, then values
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    if (gt >= kStages && !(ok = wait((v ? C_VE : C_KE) + st, (use - 1) & 1))) break;
+                    if (!(ok = wait(C_RK + v, gt & 1))) break;
+                    convert(raw + v * 128 * kD, sbase + (v ? v_off<kD>() : k_off<kD>()) + st * kTile,
+                            v && 128 * (t + 1) > keys, C_RKF + v);
+                    if (lane == 0) mbar_arrive(bar((v ? C_VF : C_KF) + st));
+                }
+                if (!ok) break;
             }
         }
     } else {
@@ -676,6 +699,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             float m_run = -CUDART_INF_F, mv_run = -CUDART_INF_F, l = 0.f;   // references of l and of O
             for (int t = 0; t < T; ++t, ++gt, ++gp) {
                 ok = mbar_wait_lazy(bar(C_SC + gt % kScaleSlots), (gt / kScaleSlots) & 1, abort_flag, a.status);
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h, vis -= 64) {
                     ok = ok && mbar_wait_lazy(bar(C_S + 2 * q + h), gp & 1, abort_flag, a.status);
                     if (!__all_sync(~0u, ok)) { ok = false; break; }
@@ -692,7 +716,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     // 16 keys share a page, so a scale: the largest logit of each
                     // group (four chains side by side)
                     const float4 *sc = scales + (gt % kScaleSlots) * 8 + 4 * h;
-                    float gm[4], sk[4], lv[4];
+                    float gm[4], sk[4], lv[4], hole[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) gm[i] = fmaxf(x[16 * i], x[16 * i + 1]);
 #pragma unroll
@@ -705,7 +729,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                         const float4 f = sc[i];
                         sk[i] = logit_scale(f.x, qf);
                         lv[i] = f.z;
-                        gm[i] *= sk[i];
+                        hole[i] = f.w;
+                        gm[i] = fmaf(gm[i], sk[i], f.w);
                         mx = fmaxf(mx, gm[i]);
                         mv = fmaxf(mv, gm[i] + lv[i]);
                     }
@@ -726,7 +751,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                             ok = mbar_wait_lazy(bar(C_PV + q), (2 * gp + h - 1) & 1, abort_flag, a.status);
                             if (!__all_sync(~0u, ok)) { ok = false; break; }
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 2
                             for (int cc = 0; cc < kD / 8; ++cc) {
                                 float o[8];
                                 tmem_ld8(tO + 8 * cc, o);
@@ -753,7 +778,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         ex[i] = fmaxf(fminf(lv[i] + vf, 100.f), -100.f);
-                        const float2 f2 = make_float2(sk[i], sk[i]), b2 = make_float2(ex[i] - ref, ex[i] - ref);
+                        const float2 f2 = make_float2(sk[i], sk[i]), b2 = make_float2(ex[i] - ref + hole[i], ex[i] - ref + hole[i]);
 #pragma unroll
                         for (int k = 16 * i; k < 16 * i + 16; k += 2) {
                             const float2 z = ffma2(make_float2(x[k], x[k + 1]), f2, b2);
@@ -808,7 +833,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : mv_run == -CUDART_INF_F ? 0.f * l : ex2(mv_run - m_run) / l;   // NaN stays NaN
             float *rec = a.rec + ((size_t)blockIdx.x * 2 + (g.out == 2 ? 1 : 0)) * (kD + 3) * 256 + 128 * q + r;
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < kD / 32; ++cc) {
                 float o[32];
                 tmem_ld32(tO + 32 * cc, o);

@@ -427,9 +427,11 @@ int sparse_attn_lsa_tree_decode(const sa_lsa_params *p, int fanout, int beam, co
  * sequence 1, ...: rows cu[b] .. cu[b + 1] - 1 belong to sequence b, cu int32
  * [B + 1].  They have `tokens` rows; rows from cu[B] on are padding, which no
  * call reads or writes unless stated.  Codes are e4m3 (append never writes its
- * NaN patterns) or int8.  A page belongs to one sequence as far as the calls below write to it;
- * the attention may read shared ones.  Status bits as for
- * sparse_attn_check_status, and 16: pages or slots ran out. */
+ * NaN patterns) or int8.  A page belongs to one sequence as far as the calls
+ * below write to it; the attention may read shared ones.  Where the attention
+ * meets a page outside 0 .. pages - 1 it sets status bit 1 and leaves the
+ * block's keys out.  Status bits as for sparse_attn_check_status, and 16:
+ * pages or slots ran out. */
 typedef struct {
     int B;          /* sequences, 1 .. 16384                                        */
     int Hq, Hkv;    /* query and key/value heads; Hq % Hkv == 0                     */
@@ -456,8 +458,8 @@ enum { SA_OP_PAGED_TABLES = 0, SA_OP_PAGED_APPEND = 1, SA_OP_PAGED_GATHER = 2, S
  * sparse_attn_workspace_size: zero-filled once when allocated, calls that
  * share one must not overlap on the GPU, and one that reported a device-side
  * timeout is zero-filled again.  Sized by B, Hq, Hkv, d, flags and tokens: a
- * workspace serves every parameter set that needs no more than it holds and
- * has the same B, Hq, Hkv and flags. */
+ * workspace serves every operation and parameter set that needs no more than
+ * it holds. */
 size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op);
 
 /* Block tables and slot maps of one step: sequence b goes from cur_len[b] to

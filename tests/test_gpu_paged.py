@@ -537,6 +537,43 @@ def test_prefill_leaves_rows_before_the_first_sequence(tokens, dtype):
         assert ((x.cpu() == 5).flatten(1).all(1) == ~rows).all()
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("tokens,dtype,d,block", [(6, "bf16", 128, 64), (300, "bf16", 128, 64), (300, "bf16", 64, 16),
+                                                  (300, "bf16", 128, 128), (6, "fp32", 64, 32)])
+def test_attention_leaves_blocks_without_a_page_out(tokens, dtype, d, block, code):
+    """Table entries out of range in the middle, at both ends and all over a sequence."""
+    lens, maxb = [700, 700, 130, 260], -(-700 // block)
+    p = sa.make_paged_params(4, 4, 2, d, block, 4 * maxb, maxb, tokens, 0, 0, dtype, code)
+    cache, codes, scale = random_cache(p, 5)
+    table = random_table(p, lens, 5)
+    spoil_tails(p, cache, table, lens)
+    bad = table.copy()
+    last = -(-700 // block) - 1
+    bad[0, [1, last - 1]] = [-1, p.pages]
+    bad[1, [0, last]] = [-2 ** 31, 2 ** 31 - 1]
+    bad[2, :-(-130 // block)] = -1
+    cu = [0, tokens // 3, tokens // 2, tokens - 1, tokens]
+    Q = torch.from_numpy(np.random.default_rng(1).standard_normal((tokens, 4, d))).to(T[dtype])
+    ws = sa.paged_workspace(p)
+    got = [sa.paged_prefill(p, Q.cuda(), i32(cu), cache, i32(bad.tolist()), i32(lens), ws)]
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_check_status(ws.data_ptr(), 0) == (sa.SA_ERR_DEVICE, 1)
+    first = Q[cu[:4]].cuda()
+    got.append(sa.paged_decode(p, first, cache, i32(bad.tolist()), i32(lens), ws))
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_check_status(ws.data_ptr(), 0) == (sa.SA_ERR_DEVICE, 1)
+    kv = [op.values(p.code, c, s) for c, s in zip(codes, scale)]
+    for b, n in enumerate(lens):
+        keep = [j for j in range(-(-n // block)) if 0 <= bad[b, j] < p.pages]
+        for t in {0, cu[b + 1] - cu[b] - 1}:
+            for h in (0, 3):
+                ref = op.decode_row(Q[cu[b] + t, h].double().numpy() * d ** -0.5, kv[0], kv[1], table[b], n, h // 2, block, 0,
+                                    keep, [0.0] * len(keep))
+                check_row(dtype, got[0][0][cu[b] + t, h], got[0][1][cu[b] + t, h], ref, n, d, (b, t, h))
+                if t == 0:
+                    check_row(dtype, got[1][0][b, h], got[1][1][b, h], ref, n, d, (b, h))
+
+
 def test_prefill_rows_are_decodes():
     """One query per sequence: the chunk call and the decode call agree."""
     lens = [5000, 64, 1]
