@@ -96,17 +96,19 @@ cudaError_t launch_paged_simt(const PagedShape &s, const void *q, const int32_t 
                               const PagedLists &l, void *o, float *lse, unsigned *status, cudaStream_t st);
 
 // The tensor-core decode: bf16, `scratch` of paged_decode_scratch bytes.  With
-// cu it takes packed chunks of few rows (paged_rows_supported; no lists).
+// cu it takes packed chunks (no lists): the sequences of up to
+// paged_rows_limit rows a kv-head (0: none, INT_MAX: all of them).
 bool paged_decode_supported(const PagedShape &s);
-bool paged_rows_supported(const PagedShape &s);
+int paged_rows_limit(const PagedShape &s);
 size_t paged_decode_scratch(const PagedShape &s, bool chunk);
 cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
                                 const PagedLists &l, void *o, float *lse, unsigned *status, void *scratch,
                                 cudaStream_t st);
-// The tensor-core chunk attention: bf16, up to 128 query heads per kv-head.
+// The tensor-core chunk attention: bf16, up to 128 query heads per kv-head; the
+// sequences of more than `few` rows a kv-head.
 bool paged_prefill_supported(const PagedShape &s);
 size_t paged_prefill_scratch(const PagedShape &s);
 cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32_t *cu, const PagedCache &c, void *O,
-                                 float *lse, unsigned *status, void *scratch, cudaStream_t st);
+                                 float *lse, int few, unsigned *status, void *scratch, cudaStream_t st);
 
 }  // namespace sa

@@ -1,5 +1,6 @@
 // paged_api.cu -- the C entry points of the paged 8-bit cache: argument
 // checks, workspace sizing, dispatch.  See include/sparse_attn.h.
+#include <limits.h>
 #include <math.h>
 
 #include "paged.cuh"
@@ -80,11 +81,13 @@ size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op) {
         case SA_OP_PAGED_APPEND:
         case SA_OP_PAGED_GATHER: return kStatusBytes;
         case SA_OP_PAGED_DECODE: return kStatusBytes + al256(paged_decode_scratch(s, false));
-        case SA_OP_PAGED_PREFILL:
-            return kStatusBytes + al256(s.tokens == 0                ? 0
-                                        : paged_rows_supported(s)    ? paged_decode_scratch(s, true)
-                                        : paged_prefill_supported(s) ? paged_prefill_scratch(s)
-                                                                     : 0);
+        case SA_OP_PAGED_PREFILL: {
+            // one kernel after the other, in the same place
+            const int few = paged_rows_limit(s);
+            const size_t rows = few > 0 ? paged_decode_scratch(s, true) : 0;
+            const size_t tiles = few < INT_MAX && s.tokens > 0 && paged_prefill_supported(s) ? paged_prefill_scratch(s) : 0;
+            return kStatusBytes + al256(rows > tiles ? rows : tiles);
+        }
         default: return 0;
     }
 }
@@ -172,11 +175,14 @@ int sparse_attn_paged_prefill(const sa_paged_params *p, const void *Q, const int
     if (ws_bytes < sparse_attn_paged_workspace_size(p, SA_OP_PAGED_PREFILL)) return SA_ERR_WORKSPACE;
     if (s.tokens == 0) return SA_OK;
     const PagedCache c{(const uint8_t *)K8, (const uint8_t *)V8, kscale, vscale, table, seq_len};
-    if (paged_rows_supported(s))
-        return launch_result(launch_paged_decode(s, Q, cu, c, PagedLists{}, O, lse, (unsigned *)ws,
-                                                 (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
+    const int few = paged_rows_limit(s);
+    if (few > 0) {
+        const int done = launch_result(launch_paged_decode(s, Q, cu, c, PagedLists{}, O, lse, (unsigned *)ws,
+                                                           (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
+        if (done != SA_OK || few == INT_MAX) return done;
+    }
     if (paged_prefill_supported(s))
-        return launch_result(launch_paged_prefill(s, Q, cu, c, O, lse, (unsigned *)ws,
+        return launch_result(launch_paged_prefill(s, Q, cu, c, O, lse, few, (unsigned *)ws,
                                                   (unsigned char *)ws + kStatusBytes, (cudaStream_t)stream));
     return launch_result(
         launch_paged_simt(s, Q, cu, c, PagedLists{}, O, lse, (unsigned *)ws, (cudaStream_t)stream));

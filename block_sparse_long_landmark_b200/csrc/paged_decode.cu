@@ -33,6 +33,7 @@
 // of the largest.  P is rounded to fp16 (2^-11 of each weight; the reference
 // max is raised only when a logit passes it by 2^8, so p stays below 2^8).
 #include <cuda.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include "paged.cuh"
@@ -68,6 +69,7 @@ struct DecArgs {
     const int32_t *cu;   // packed chunk rows, or null: one query per sequence
     int lists, units;    // B * Hsel lists; the most units (groups of a list's rows) there can be
     int ranges;          // warps of the grid
+    int limit;           // chunk: lists of more rows are left to the tiles
     int group;           // rows per group
     int sub, rows, pps;  // stage geometry: parts per page, rows per part, parts per stage
 };
@@ -174,7 +176,7 @@ __device__ __forceinline__ int sees(const DecArgs &a, const ListAt &l, int r) {
     return !a.cu || !(a.s.flags & SA_CAUSAL) ? l.n : l.n - l.T + r / a.s.G + 1;
 }
 __device__ __forceinline__ int groups_of(const DecArgs &a, const ListAt &l) {
-    return (l.rows + a.group - 1) / a.group;
+    return l.rows > a.limit ? 0 : (l.rows + a.group - 1) / a.group;
 }
 
 // Entries (blocks) of a unit: its list's, or every block that one of its rows
@@ -838,6 +840,7 @@ paged_merge_kernel(DecArgs a) {
     __shared__ float part[kGroups > 1 ? kGroups - 1 : 1][kSlices][K + 2 * H][32];
     const int u = blockIdx.x, lane = threadIdx.x & 31, slice = (threadIdx.x >> 5) % kSlices;
     const int grp = threadIdx.x / (32 * kSlices), i0 = slice * K;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 in = a.info[u];
     // a range whose wait ran out may have left the entry of another call
@@ -970,8 +973,10 @@ int rows_per_group(const PagedShape &s, bool chunk) { return chunk ? 8 * head_ti
 // sequences on the device.
 long long units_of(const PagedShape &s, bool chunk) {
     const int group = rows_per_group(s, chunk);
-    return chunk ? ((long long)s.tokens * s.G / group + s.B) * s.Hkv
-                 : (long long)s.B * s.Hsel * ((s.heads_per + group - 1) / group);
+    if (!chunk) return (long long)s.B * s.Hsel * ((s.heads_per + group - 1) / group);
+    const long long any = (long long)s.tokens * s.G / group + s.B;
+    const int limit = paged_rows_limit(s);
+    return min(any, limit == INT_MAX ? any : (long long)s.B * ((limit + group - 1) / group)) * s.Hkv;
 }
 size_t rec_bytes(const PagedShape &s, bool chunk) {
     return (size_t)(s.d / 16 * 4 + 4) * head_tiles(s, chunk) * 32 * sizeof(float);
@@ -1002,13 +1007,24 @@ bool paged_decode_supported(const PagedShape &s) {
     return s.dtype == SA_BF16 && !((s.flags & SA_HIER) && s.bs > 64);
 }
 
-// A chunk of few rows reads the cache once per 16 of them here, at the decode's
+// A sequence of few rows is read once per 16 of them here, at the decode's
 // rate; the tiles of paged_prefill.cu take 256 rows in about twice the time of
-// one pass, so up to some 40 rows a sequence are better off here (8 sequences
-// of 5000 keys with 20 rows per kv-head: 42 us against 56; 64 of 16K with 16
-// rows: 239 against 677).
-bool paged_rows_supported(const PagedShape &s) {
-    return s.dtype == SA_BF16 && s.tokens > 0 && rows_per_list(s, true) <= 40 && (long long)s.tokens * s.G < (1ll << 30);
+// one such pass, so up to some 40 rows a kv-head are better off here (8
+// sequences of 5000 keys with 20 rows: 42 us against 56; 64 of 4000 with 40:
+// 306 against 412).  How the rows are shared out is known on the device only.
+// Most calls run both kernels, each over its own sequences: 512 + 63 x 1 tokens
+// over 64 x 16K keys take 542 us, all of them here 1090, all in tiles 1685.  The
+// tile kernel's three launches cost up to 20 us when no sequence is theirs (64 x
+// 4 tokens at 4000 keys 144 us with, 123 without), so a call of few rows, on
+// average (16) and in all (1024: what one long chunk among them can cost), runs
+// here as a whole.
+int paged_rows_limit(const PagedShape &s) {
+    constexpr int kFew = 40;
+    const long long rows = (long long)s.tokens * s.G;
+    if (s.dtype != SA_BF16 || s.tokens <= 0 || rows >= (1ll << 30)) return 0;
+    if (s.G > 128) return INT_MAX;
+    if (s.B == 1) return rows <= kFew ? INT_MAX : 0;
+    return rows <= max(256, min(16 * s.B, 1024)) ? INT_MAX : kFew;
 }
 
 size_t paged_decode_scratch(const PagedShape &s, bool chunk) {
@@ -1032,6 +1048,7 @@ cudaError_t launch_paged_decode(const PagedShape &shape, const void *q, const in
     a.c = c;
     a.l = l;
     a.cu = cu;
+    a.limit = chunk ? paged_rows_limit(s) : INT_MAX;
     a.q = (const __nv_bfloat16 *)q;
     a.o = (__nv_bfloat16 *)o;
     a.lse = lse;

@@ -94,6 +94,7 @@ struct PreArgs {
     float *rec;         // [grid][2][d + 3][256]: O, m, l, m'
     int tpt;            // tokens per 128-row tile
     int box;            // rows of one copy: 16 to 128 keys of one page
+    int few;            // sequences of up to so many rows a kv-head are done elsewhere
 };
 
 struct Seg {
@@ -143,6 +144,11 @@ __device__ __forceinline__ void rows_of(const PreArgs &a, int b, int &r0, int &r
     r1 = max(r0, min(a.cu[b + 1], a.s.tokens));
 }
 
+// Units of a sequence's rows r0 .. r1 - 1.
+__device__ __forceinline__ int units_in(const PreArgs &a, int r0, int r1) {
+    return (long long)(r1 - r0) * a.s.G <= a.few ? 0 : (r1 - r0 + 2 * a.tpt - 1) / (2 * a.tpt);
+}
+
 __global__ void __launch_bounds__(1024)
 paged_plan_kernel(PreArgs a) {
     extern __shared__ int off_s[];
@@ -187,7 +193,7 @@ paged_plan_kernel(PreArgs a) {
     for (int b = b0; b < b1; ++b) {
         int r0, r1;
         rows_of(a, b, r0, r1);
-        n += (r1 - r0 + tpu - 1) / tpu;
+        n += units_in(a, r0, r1);
         if (!(a.cu[b] >= 0 && a.cu[b] <= a.cu[b + 1] && a.cu[b + 1] <= s.tokens)) bad_s = 1;
     }
     long long at = scan1024(n, tmp, total) - n;
@@ -197,7 +203,7 @@ paged_plan_kernel(PreArgs a) {
         int r0, r1;
         rows_of(a, b, r0, r1);
         off_s[b] = bad ? 0 : (int)at;
-        at += (r1 - r0 + tpu - 1) / tpu;
+        at += units_in(a, r0, r1);
     }
     __syncthreads();
     const int units = bad ? 0 : (int)total;
@@ -953,8 +959,9 @@ size_t paged_prefill_scratch(const PagedShape &s) {
 }
 
 cudaError_t launch_paged_prefill(const PagedShape &s, const void *Q, const int32_t *cu, const PagedCache &c, void *O,
-                                 float *lse, unsigned *status, void *scratch, cudaStream_t st) {
+                                 float *lse, int few, unsigned *status, void *scratch, cudaStream_t st) {
     PreArgs a{};
+    a.few = few;
     a.s = s;
     a.c = c;
     a.cu = cu;

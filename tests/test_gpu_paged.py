@@ -466,6 +466,17 @@ def test_prefill_of_few_rows(causal, code, d, block, Hq, Hkv, grown):
     run_chunks(causal, code, "bf16", d, block, Hq, Hkv, grown)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("code,d,block,Hq,Hkv,grown", [
+    ("e4m3", 128, 64, 8, 2, [150, 0, 1, 10, 11, 3, 0]), ("int8", 64, 16, 5, 1, [1, 0, 1, 8, 9, 200, 1]),
+    ("int8", 128, 48, 24, 2, [3, 0, 1, 4, 2, 90, 4]), ("e4m3", 128, 112, 40, 1, [1, 0, 1, 2, 1, 1, 60]),
+    ("e4m3", 64, 64, 132, 1, [9, 0, 1, 2, 1, 5, 0])])
+def test_prefill_of_a_mixed_batch(causal, code, d, block, Hq, Hkv, grown):
+    """Single tokens and drafts beside a prompt's chunk: sequences of up to 40
+    rows a kv-head and of more are taken by different kernels."""
+    run_chunks(causal, code, "bf16", d, block, Hq, Hkv, grown)
+
+
 def run_chunks(causal, code, dtype, d, block, Hq, Hkv, grown):
     lens = [300, 0, 1, 257, 40, 600, 130]
     grown = list(grown)
