@@ -38,7 +38,7 @@
 // The warps' loops share the instruction caches, so code is kept short: with
 // the issuers', converters', rescaling and epilogue loops unrolled, 114 KB, a 4K
 // chunk at 32K took 2.32 ms and any line more or less moved it by 10 %; rolled,
-// 78 KB, 2.11 ms, and it holds still.
+// 78 KB, 2.1 to 2.2 ms, and it holds still.
 // Registers: launched at 128; 112 + 112 + 2 * 144 = 4 * 128.
 // Every wait is bounded; when one runs out the CTA sets the status word, lets
 // its copies land, frees tensor memory and exits.
