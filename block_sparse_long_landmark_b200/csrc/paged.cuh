@@ -22,6 +22,15 @@ struct PagedShape {
     float scale;
 };
 
+// Softmax weights of the tensor-core forms are fp16, 2^(z - reference).  The
+// reference is raised only when a logit passes it by kWeightLift + kWeightSlack,
+// to kWeightLift below that logit: weights stay below 2^15 (fp16 holds 2^16), and
+// one that falls below fp16's normal range is off by 2^-25 2^-kWeightLift = 2^-32
+// of the row's largest at most.  With the reference at the largest logit (2^-25)
+// a row whose weight lies on one key without a value (a sink) lost what the
+// others left of it: all of it at 2^-27.  No instruction more.
+constexpr float kWeightLift = 7.f, kWeightSlack = 8.f;
+
 // Cache length of sequence b, clamped to [0, maxb * bs].
 __device__ __forceinline__ int paged_len(const PagedShape &s, const int32_t *seq_len, int b) {
     return min(max(seq_len[b], 0), s.maxb * s.bs);

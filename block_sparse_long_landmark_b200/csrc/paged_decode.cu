@@ -30,8 +30,9 @@
 //     form rows 0-7 and 8-15.
 // fp16 queries: each row is scaled by a power of two so that its largest
 // element lies in [2^14, 2^15); what falls below fp16's range is under 2^-38
-// of the largest.  P is rounded to fp16 (2^-11 of each weight; the reference
-// max is raised only when a logit passes it by 2^8, so p stays below 2^8).
+// of the largest.  P is rounded to fp16: half a step, 2^-11, of each weight, or
+// 2^-32 of the row's largest where that is more (kWeightLift in paged.cuh); the
+// sum counts the weights before they are rounded.
 #include <cuda.h>
 #include <limits.h>
 #include <math_constants.h>
@@ -668,7 +669,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (!hier) {
             bool high = false;
 #pragma unroll
-            for (int i = 0; i < 2 * kNT; ++i) high |= top[i] > acc.m[i] + 8.f;
+            for (int i = 0; i < 2 * kNT; ++i) high |= top[i] > acc.m[i] + (kWeightLift + kWeightSlack);
             if (__any_sync(~0u, high)) {
                 float f[2 * kNT];
 #pragma unroll
@@ -677,7 +678,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                    x = fmaxf(x, acc.m[i]);
+                    x = fmaxf(x - kWeightLift, acc.m[i]);
                     f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - x);
                     acc.m[i] = x;
                     acc.l[i] *= f[i];
@@ -720,7 +721,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 f[i] = 1.f;
                 pf[i] = 0.f;
                 if (lb > 0.f) {
-                    const float M = fmaxf(acc.m[i], score);
+                    // nothing is held back here: the weights get all the room
+                    const float M = fmaxf(acc.m[i], score - (kWeightLift + kWeightSlack));
                     f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - M);
                     const float w = ex2(score - M);
                     acc.m[i] = M;

@@ -17,11 +17,13 @@
 //     largest element lies in [2^14, 2^15): what falls below fp16's range is
 //     under 2^-38 of it.  Scales stay out of the matrices: the key's and the
 //     row's multiply the logit, the value's the weight;
-//   * weights are rounded to fp16 (2^-11 of each).  p vs spans the scales'
-//     range, so O has a reference of its own: with m the row's largest logit
-//     and m' its largest logit + log2 vs, l sums p = 2^(z - m) and the tensor
-//     core gets p vs 2^(m - m'), at most 2^8 (references are raised when a
-//     logit passes them by 2^8), whatever the scales;
+//   * weights are rounded to fp16.  p vs spans the scales' range, so O has a
+//     reference of its own: with m the row's largest logit and m' its largest
+//     logit + log2 vs, less kWeightLift, l sums p = 2^(z - m) unrounded and the
+//     tensor core gets p vs 2^(m - m'), below 2^15 whatever the scales (a
+//     reference is raised once it is passed by 2^8 more than it was raised
+//     for).  Rounding is off by half a step, 2^-11, of a p vs, or 2^-32 of the
+//     row's largest where that is more;
 //   * S of a key tile comes in two halves of 64 keys with a buffer each, so
 //     the tensor core fills one while the softmax empties the other (one S of
 //     128 keys left the softmax waiting 30 % of the time);
@@ -740,11 +742,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                         mx = fmaxf(mx, gm[i]);
                         mv = fmaxf(mv, gm[i] + lv[i]);
                     }
-                    const bool need = mx > m_run + 8.f || mv > mv_run + 8.f;
+                    const bool need = mx > m_run + kWeightSlack || mv > mv_run + (kWeightLift + kWeightSlack);
                     if (__any_sync(~0u, need)) {
                         float corr = 1.f;
                         if (need) {
-                            const float m1 = fmaxf(mx, m_run), v1 = fmaxf(mv, mv_run);
+                            const float m1 = fmaxf(mx, m_run), v1 = fmaxf(mv - kWeightLift, mv_run);
                             l *= m_run == m1 ? 1.f : ex2(m_run - m1);
                             corr = mv_run == v1 ? 1.f : ex2(mv_run - v1);
                             m_run = m1;

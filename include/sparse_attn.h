@@ -431,7 +431,12 @@ int sparse_attn_lsa_tree_decode(const sa_lsa_params *p, int fanout, int beam, co
  * below write to it; the attention may read shared ones.  Where the attention
  * meets a page outside 0 .. pages - 1 it sets status bit 1 and leaves the
  * block's keys out.  Status bits as for sparse_attn_check_status, and 16:
- * pages or slots ran out. */
+ * pages or slots ran out.
+ * Logits, softmax sums and outputs are held in fp32.  With SA_BF16 the softmax
+ * weights enter the product with the values in fp16, off by 2^-11 of each or by
+ * 2^-32 of the row's largest where that is more, and so do the queries, exactly
+ * down to 2^-31 of a row's largest element.  SA_FP32, and hierarchical lists
+ * over blocks above 64, round neither. */
 typedef struct {
     int B;          /* sequences, 1 .. 16384                                        */
     int Hq, Hkv;    /* query and key/value heads; Hq % Hkv == 0                     */
