@@ -774,9 +774,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     }
                     // w = p vs 2^(m - m') = 2^(z - m + e), e = log2 vs + m - m'
                     // of the group: one exponential a key; l gets the group's
-                    // sum times 2^-e.  The limits on e keep 2^-e and the
-                    // exponential finite; at vs = 0 (e = -100) w vanishes in
-                    // fp16 and l loses only what is under 2^-26 of the row.
+                    // sum times 2^-e.  Limits on e keep 2^-e and the exponential
+                    // finite and change no result: at e = -40 (vs = 0) w
+                    // vanishes in fp16 and l still counts p down to 2^-86; above
+                    // 300, where l takes nothing any more (p is under 2^-285),
+                    // the output is under fp32's range.  (With a limit of 100,
+                    // values of scale 2^40 a hundred bits below a page without
+                    // any came out 2^10 too small.)
                     const float ref = m_run == -CUDART_INF_F ? 0.f : m_run;
                     const float vf = mv_run == -CUDART_INF_F ? 0.f : ref - mv_run;
                     // The 16-key groups run as a pipeline: a group's exponentials
@@ -785,7 +789,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     float ex[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        ex[i] = fmaxf(fminf(lv[i] + vf, 100.f), -100.f);
+                        ex[i] = fmaxf(fminf(lv[i] + vf, 300.f), -40.f);
                         const float2 f2 = make_float2(sk[i], sk[i]), b2 = make_float2(ex[i] - ref + hole[i], ex[i] - ref + hole[i]);
 #pragma unroll
                         for (int k = 16 * i; k < 16 * i + 16; k += 2) {

@@ -107,3 +107,65 @@ def test_weights_far_below_the_largest(form, n, bits, code):
         for h in (0, 3):
             ref = op.decode_row(Q[t, h].double().numpy() * d ** -0.5, *vals, table[0], n, 0, block, flags, idx, sc)
             check_close("bf16", O[t, h], lse[t, h], ref, n, d, floor, (t, h))
+
+
+# ---- value scales far apart -------------------------------------------------------------
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,where", [(300, "first"), (300, "last"), (300, "all"), (1500, "first"), (1500, "middle")])
+@pytest.mark.parametrize("tokens", [ROWS, TILES])
+def test_value_scales_of_zero_and_far_apart(tokens, n, where, code):
+    """Pages with a value scale of 0 at either end and all over, the others
+    spread over 2^60; tiny and huge queries."""
+    d, block, Hq = 128, 32, 4
+    maxb = -(-n // block)
+    p = sa.make_paged_params(1, Hq, 1, d, block, maxb, maxb, tokens, flags=sa.SA_CAUSAL, code=code)
+    rng = np.random.default_rng(n)
+    codes = [op.encode(p.code, rng.standard_normal((maxb, 1, block, d)) * 40) for _ in "kv"]
+    ks, vs = rng.uniform(1e-4, 3e-3, (maxb, 1)), 2.0 ** rng.uniform(-30, 30, (maxb, 1))
+    vs[{"first": slice(0, 5), "last": slice(maxb - 5, maxb), "all": slice(0, maxb), "middle": slice(9, 20)}[where]] = 0
+    ks, vs = ks.astype(np.float32), vs.astype(np.float32)
+    cache = cache_of(p, codes, (ks, vs))
+    Q = torch.from_numpy(rng.standard_normal((tokens, Hq, d)) * 2.0 ** rng.integers(-4, 5, (tokens, Hq, 1)))
+    Q[0, 0] *= 2.0 ** -100
+    Q[0, 1] *= 2.0 ** 8
+    Q = Q.bfloat16()
+    ws = sa.paged_workspace(p)
+    O, lse = sa.paged_prefill(p, Q.cuda(), i32([0, tokens]), cache, i32([list(range(maxb))]), i32([n]), ws)
+    done(ws)
+    kv = [op.values(p.code, c, s) for c, s in zip(codes, (ks, vs))]
+    for t in {0, 1, tokens // 2, tokens - 1}:
+        see = n - tokens + t + 1
+        for h in range(Hq):
+            q = Q[t, h].double().numpy() * d ** -0.5
+            ref = op.decode_row(q, *kv, list(range(maxb)), see, 0, block, 0)
+            # the tiles round a weight times its value's scale
+            floor = 2.0 ** -32 * float(vs.max()) * np.abs(op.decode_codes(p.code, codes[1])).sum((0, 1, 2))
+            check_close("bf16", O[t, h], lse[t, h], ref, see, d, floor, (t, h))
+
+
+@pytest.mark.parametrize("bits,up,zero", [(60, 40, -60), (110, 40, -100), (120, 60, -126), (20, 60, 0), (115, 90, -40)])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_tiles_join_what_value_scales_set_apart(code, bits, up, zero):
+    """A block of no value takes the weight (its scale is tiny, or 0), and what
+    lies 2^bits below has values of scale 2^up: the row is what that leaves."""
+    n, d, block, Hq, tokens = 192, 64, 64, 4, TILES
+    p = sa.make_paged_params(1, Hq, 1, d, block, 3, 3, tokens, code=code)
+    codes, (ks, vs), q = sink_row(p, code, n, bits, 3)
+    vs[:] = 2.0 ** up
+    codes[1][0] = 0
+    vs[0] = 2.0 ** zero if zero else 0.0
+    cache = cache_of(p, codes, (ks, vs))
+    Q = torch.from_numpy(q).bfloat16().repeat(tokens, 1, 1)
+    ws = sa.paged_workspace(p)
+    O, lse = sa.paged_prefill(p, Q.cuda(), i32([0, tokens]), cache, i32([[0, 1, 2]]), i32([n]), ws)
+    done(ws)
+    kv = [op.values(p.code, c, s.astype(np.float32)) for c, s in zip(codes, (ks, vs))]
+    raws = op.decode_codes(p.code, codes[1])[:, 0].reshape(-1, d)
+    for t, h in ((0, 0), (33, 1), (tokens - 1, 3)):
+        qd = Q[t, h].double().numpy() * d ** -0.5
+        ref = op.decode_row(qd, *kv, [0, 1, 2], n, 0, block, 0)
+        z = kv[0][:, 0].reshape(-1, d) @ qd
+        w = np.exp(z - z.max()) * np.repeat(vs[:, 0], block)
+        floor = 2.0 ** -32 * w.max() * np.abs(raws).sum(0)        # a weight times its value's scale is what is rounded
+        check_close("bf16", O[t, h], lse[t, h], ref, n, d, floor, (t, h))
