@@ -169,3 +169,116 @@ def test_tiles_join_what_value_scales_set_apart(code, bits, up, zero):
         w = np.exp(z - z.max()) * np.repeat(vs[:, 0], block)
         floor = 2.0 ** -32 * w.max() * np.abs(raws).sum(0)        # a weight times its value's scale is what is rounded
         check_close("bf16", O[t, h], lse[t, h], ref, n, d, floor, (t, h))
+
+
+# ---- ranges of many steps ------------------------------------------------------------------
+
+def pooled_cache(p, seed):
+    """A cache of drawn codes, quickly made, with scales that differ."""
+    rng = np.random.default_rng(seed)
+    pool = op.encode(p.code, rng.standard_normal(1 << 16) * (60 if p.code == op.E4M3 else 30))
+    shape = (p.pages, p.Hkv, p.block, p.d)
+    codes = [pool[rng.integers(0, 1 << 16, shape)] for _ in "kv"]
+    scales = [rng.uniform(0.004, 0.03, shape[:2]).astype(np.float32) for _ in "kv"]
+    return cache_of(p, codes, scales), [op.values(p.code, c, s) for c, s in zip(codes, scales)]
+
+
+def sms():
+    return min(148, torch.cuda.get_device_properties(0).multi_processor_count)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("code,d,block,Hq,Hkv", [("e4m3", 128, 64, 32, 8), ("int8", 128, 48, 40, 8),
+                                                 ("int8", 64, 16, 24, 8), ("e4m3", 64, 128, 32, 8)])
+def test_tiles_of_many_steps(code, d, block, Hq, Hkv, causal):
+    """Every CTA walks through twenty key tiles and more, units of one and of
+    two query tiles after one another; the pages are shared, as they may be."""
+    lens, grown = [9000, 16000, 12345, 100, 9999], [300, 2048, 30, 72, 33]
+    G, maxb = Hq // Hkv, -(-16000 // block)
+    tpu = 2 * (128 // G)
+    tiles = sum(-(-(min(n, n - g + min(g, t + tpu)) if causal else n) // 128) for n, g in zip(lens, grown) for t in range(0, g, tpu))
+    assert tiles * Hkv >= 20 * sms() and any(0 < g % tpu <= tpu // 2 for g in grown)
+    cu = [sum(grown[:i]) for i in range(6)]
+    p = sa.make_paged_params(5, Hq, Hkv, d, block, 150, maxb, cu[-1] + 3, flags=sa.SA_CAUSAL if causal else 0, code=code)
+    cache, kv = pooled_cache(p, 1)
+    rng = np.random.default_rng(2)
+    table = rng.integers(0, p.pages, (5, maxb)).astype(np.int32)
+    Q = torch.from_numpy(rng.standard_normal((p.tokens, Hq, d)) * rng.choice([1.0, 6.0], (p.tokens, Hq, 1))).bfloat16()
+    ws = sa.paged_workspace(p)
+    O, lse = sa.paged_prefill(p, Q.cuda(), i32(cu), cache, i32(table.tolist()), i32(lens), ws)
+    done(ws)
+    for b, (n, g) in enumerate(zip(lens, grown)):
+        for t in sorted({0, 63, g // 3, g // 2, g - 65, g - 1} & set(range(g))):
+            for h in (t % Hq, (t + 5 * b + 9) % Hq):
+                see = n - g + t + 1 if causal else n
+                ref = op.decode_row(Q[cu[b] + t, h].double().numpy() * d ** -0.5, *kv, table[b], see, h // G, block, 0)
+                floor = 2.0 ** -32 * np.abs(op.rows_of(kv[1], table[b], see, h // G, block)).sum(0)
+                check_close("bf16", O[cu[b] + t, h], lse[cu[b] + t, h], ref, see, d, floor, (b, t, h))
+
+
+@pytest.mark.parametrize("form", ["decode", "rows"])
+@pytest.mark.parametrize("code,d,block,Hq,Hkv", [("e4m3", 128, 64, 32, 8), ("int8", 128, 16, 32, 8),
+                                                 ("int8", 64, 112, 80, 8), ("e4m3", 64, 32, 16, 8)])
+def test_steps_of_many_stages(code, d, block, Hq, Hkv, form):
+    """Every warp streams thirty stages and more: more than one batch of parts,
+    every place of the stage memory used again and again."""
+    B = 32
+    lens = [16000 - 97 * b for b in range(B)]
+    G, maxb = Hq // Hkv, -(-16000 // block)
+    grown = [1 + b % 3 for b in range(B)]
+    T_ = sum(grown) if form == "rows" else 0
+    assert sum(-(-n // 64) for n in lens) * Hkv >= 30 * sms() * 12
+    p = sa.make_paged_params(B, Hq, Hkv, d, block, 150, maxb, T_, flags=sa.SA_CAUSAL, code=code)
+    cache, kv = pooled_cache(p, 1)
+    rng = np.random.default_rng(2)
+    table = rng.integers(0, p.pages, (B, maxb)).astype(np.int32)
+    cu = [sum(grown[:i]) for i in range(B + 1)]
+    Q = torch.from_numpy(rng.standard_normal((T_ or B, Hq, d)) * 2.0 ** rng.integers(-1, 3, (T_ or B, Hq, 1))).bfloat16()
+    ws = sa.paged_workspace(p)
+    args = cache, i32(table.tolist()), i32(lens), ws
+    O, lse = sa.paged_prefill(p, Q.cuda(), i32(cu), *args) if T_ else sa.paged_decode(p, Q.cuda(), *args)
+    done(ws)
+    for b in range(0, B, 3):
+        for t in range(grown[b] if T_ else 1):
+            for h in ((b + t) % Hq, (b + 7 * t + 11) % Hq):
+                row, see = (cu[b] + t, lens[b] - grown[b] + t + 1) if T_ else (b, lens[b])
+                ref = op.decode_row(Q[row, h].double().numpy() * d ** -0.5, *kv, table[b], see, h // G, block, 0)
+                floor = 2.0 ** -32 * np.abs(op.rows_of(kv[1], table[b], see, h // G, block)).sum(0)
+                check_close("bf16", O[row, h], lse[row, h], ref, see, d, floor, (b, t, h))
+
+
+# ---- one value row decides ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("tokens,d,block", [(0, 128, 64), (0, 64, 112), (0, 128, 16), (ROWS, 64, 48), (ROWS, 128, 128),
+                                            (TILES, 128, 64), (TILES, 64, 48), (TILES, 128, 16), (TILES, 64, 128)])
+def test_one_value_row_decides(tokens, d, block, code):
+    """All values but one key's are zero, for keys at the ends of tiles, pages
+    and the sequence: a row in the wrong place, or a wrong scale, is the whole output."""
+    n, Hq = 5 * 128 + 37, 4
+    keys = sorted({0, 15, 16, 63, 64, 127, 128, 255, 256, 383, 575, 576, 639, 640, n - 6, n - 1, block - 1, block,
+                   n // block * block - 1, n // block * block})
+    maxb, B = -(-n // block), len(keys)
+    p = sa.make_paged_params(B, Hq, 1, d, block, B * maxb, maxb, tokens * B, code=code)
+    cache, kv = pooled_cache(p, 4)
+    table = random_table(p, [n] * B, 4)
+    vals = raw(cache[1])
+    keep = np.zeros(vals.shape, bool)
+    for b, j in enumerate(keys):
+        keep[table[b, j // block], 0, j % block] = True
+    vals[~keep] = 0
+    cache = (cache[0], torch.from_numpy(vals).cuda().view(cache[1].dtype), *cache[2:])
+    kv[1] = op.values(p.code, vals, cache[3].cpu().numpy())
+    Q = torch.from_numpy(np.random.default_rng(3).standard_normal((tokens * B or B, Hq, d)) / 3).bfloat16()
+    ws = sa.paged_workspace(p)
+    args = cache, i32(table.tolist()), i32([n] * B), ws
+    if tokens:
+        O, lse = sa.paged_prefill(p, Q.cuda(), i32([tokens * b for b in range(B + 1)]), *args)
+    else:
+        O, lse = sa.paged_decode(p, Q.cuda(), *args)
+    done(ws)
+    for b in range(B):
+        for t in {0, tokens // 2, tokens - 1} if tokens else {0}:
+            row = b * max(1, tokens) + t
+            ref = op.decode_row(Q[row, 1].double().numpy() * d ** -0.5, *kv, table[b], n, 0, block, 0)
+            check_close("bf16", O[row, 1], lse[row, 1], ref, n, d, 2.0 ** -32 * np.abs(kv[1]).max((0, 1, 2)), (keys[b], t))
