@@ -282,3 +282,27 @@ def test_one_value_row_decides(tokens, d, block, code):
             row = b * max(1, tokens) + t
             ref = op.decode_row(Q[row, 1].double().numpy() * d ** -0.5, *kv, table[b], n, 0, block, 0)
             check_close("bf16", O[row, 1], lse[row, 1], ref, n, d, 2.0 ** -32 * np.abs(kv[1]).max((0, 1, 2)), (keys[b], t))
+
+
+# ---- queries that are not numbers, block by block -------------------------------------------
+
+@pytest.mark.parametrize("dtype,block", [("bf16", 64), ("bf16", 16), ("bf16", 128), ("fp32", 64)])
+def test_hierarchical_decode_keeps_a_query_that_is_not_a_number(dtype, block):
+    """Its row's output is NaN, its lse the lists' alone; other rows are untouched."""
+    lens, maxb = [500, 321], -(-500 // block)
+    p = sa.make_paged_params(2, 8, 2, 128, block, 2 * maxb, maxb, 0, 3, sa.SA_SINK | sa.SA_LOCAL | sa.SA_HIER, dtype)
+    cache, _ = pooled_cache(p, 2)
+    table, n, ws = i32(random_table(p, lens, 2).tolist()), i32(lens), sa.paged_workspace(p)
+    idx, cnt = i32([[[0, 1, -(-m // block) - 1, -1, -1]] * 2 for m in lens]), i32([[3, 3]] * 2)
+    sc = torch.randn(2, 2, 5, device="cuda")
+    q = torch.randn(2, 8, 128, device="cuda").to(T[dtype])
+    bad = q.clone()
+    bad[0, 3, 7], bad[1, 0, 0] = math.nan, math.inf
+    o, lse = sa.paged_decode(p, q, cache, table, n, ws, lists=(idx, sc, cnt))
+    o2, lse2 = sa.paged_decode(p, bad, cache, table, n, ws, lists=(idx, sc, cnt))
+    done(ws)
+    keep = torch.ones(2, 8, dtype=torch.bool, device="cuda")
+    keep[0, 3] = keep[1, 0] = False
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert torch.isnan(o2[~keep].float()).all() and not torch.isnan(o.float()).any()
+    assert torch.equal(lse, lse2)
