@@ -153,7 +153,8 @@ paged_simt_kernel(SimtArgs a, const T *__restrict__ q, T *__restrict__ o, float 
                 for (int i = 0; i < DL; ++i) st.acc[i] = fmaf(w, code_value<kCode>(vr[i]), st.acc[i]);
             }
         }
-        if (hier && blkst.l != 0.f) {       // 0: no key; NaN goes on
+        // no key (NaN goes on), or no weight
+        if (hier && blkst.l != 0.f && sc[e] != -CUDART_INF_F) {
             const float w2 = sc[e] * kLog2e;
             if (w2 > run.m) run.raise(w2);
             const float w = exp2f(w2 - run.m);

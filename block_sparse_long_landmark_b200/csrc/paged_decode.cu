@@ -720,7 +720,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 lb += __shfl_xor_sync(~0u, lb, 16);
                 f[i] = 1.f;
                 pf[i] = 0.f;
-                if (lb != 0.f) {        // 0: no key; a query that is not a number goes on
+                // 0: no key (a query that is not a number goes on); -inf: no weight
+                if (lb != 0.f && score != -CUDART_INF_F) {
                     // nothing is held back here: the weights get all the room
                     const float M = fmaxf(acc.m[i], score - (kWeightLift + kWeightSlack));
                     f[i] = acc.m[i] == -CUDART_INF_F ? 0.f : ex2(acc.m[i] - M);

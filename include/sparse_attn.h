@@ -522,8 +522,8 @@ int sparse_attn_paged_gather(const sa_paged_params *p, const int64_t *slot, cons
  * from sparse_attn_select_decode_varlen with N = max_blocks * block): the kept
  * blocks, gated, hierarchical or plain as in sparse_attn_decode_varlen.
  * Without (idx, score and count NULL): every block of the sequence; SA_GATE
- * and SA_HIER are SA_ERR_UNSUPPORTED then.  A sequence of length 0 or without
- * a block gives o = 0, lse = -inf. */
+ * and SA_HIER are SA_ERR_UNSUPPORTED then.  A block whose score is -inf has no
+ * weight; a sequence of length 0 or without a block gives o = 0, lse = -inf. */
 int sparse_attn_paged_decode(const sa_paged_params *p, const void *q, const void *K8, const void *V8,
                              const float *kscale, const float *vscale, const int32_t *table, const int32_t *seq_len,
                              const int32_t *idx, const float *score, const int32_t *count, void *o, float *lse,

@@ -306,3 +306,28 @@ def test_hierarchical_decode_keeps_a_query_that_is_not_a_number(dtype, block):
     assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
     assert torch.isnan(o2[~keep].float()).all() and not torch.isnan(o.float()).any()
     assert torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype,block", [("bf16", 64), ("bf16", 128), ("fp32", 16)])
+@pytest.mark.parametrize("where", [[0], [1], [2], [0, 1], [0, 1, 2]])
+def test_hierarchical_blocks_of_no_weight(dtype, block, where):
+    """A block whose score is -inf takes no part, the first ones and all of them too."""
+    n, maxb = 500, -(-500 // block)
+    p = sa.make_paged_params(1, 4, 1, 128, block, maxb, maxb, 0, 3, sa.SA_SINK | sa.SA_LOCAL | sa.SA_HIER, dtype)
+    cache, kv = pooled_cache(p, 2)
+    table, ws = random_table(p, [n], 2), sa.paged_workspace(p)
+    idx, sc = [0, 1, maxb - 1, -1, -1], np.zeros(5, np.float32)
+    sc[:3] = [0.3, -1.0, 2.0]
+    sc[where] = -math.inf
+    q = torch.randn(1, 4, 128, device="cuda").to(T[dtype])
+    o, lse = sa.paged_decode(p, q, cache, i32(table.tolist()), i32([n]), ws,
+                             lists=(i32([[idx]]), torch.from_numpy(sc).cuda()[None, None], i32([[3]])))
+    done(ws)
+    live = [i for i in range(3) if i not in where]
+    if not live:
+        assert not o.any() and torch.isneginf(lse).all()
+        return
+    for h in range(4):
+        ref = op.decode_row(q[0, h].double().cpu().numpy() * 128 ** -0.5, *kv, table[0], n, 0, block, p.flags,
+                            [idx[i] for i in live], sc[live])
+        check_close(dtype, o[0, h], lse[0, h], ref, n, 128, 2.0 ** -32 * np.abs(kv[1]).sum((0, 1, 2)), h)
