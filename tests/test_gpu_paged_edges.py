@@ -331,3 +331,24 @@ def test_hierarchical_blocks_of_no_weight(dtype, block, where):
         ref = op.decode_row(q[0, h].double().cpu().numpy() * 128 ** -0.5, *kv, table[0], n, 0, block, p.flags,
                             [idx[i] for i in live], sc[live])
         check_close(dtype, o[0, h], lse[0, h], ref, n, 128, 2.0 ** -32 * np.abs(kv[1]).sum((0, 1, 2)), h)
+
+
+# ---- a flag that only lists have a use for -------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d,block,Hq,Hkv", [("bf16", 128, 64, 32, 8), ("bf16", 64, 16, 40, 2), ("bf16", 128, 128, 24, 1),
+                                                  ("fp32", 64, 32, 8, 2)])
+def test_dense_decode_of_lists_per_query_head(dtype, d, block, Hq, Hkv):
+    """Without lists, SA_SELECT_PER_QHEAD changes nothing: a kv-head's query
+    heads read its cache together, in the same order of sums."""
+    lens = [9000, 5, 0, 2500]
+    maxb = -(-9000 // block)
+    a, b = (sa.make_paged_params(4, Hq, Hkv, d, block, 200, maxb, flags=f, dtype=dtype) for f in (0, sa.SA_SELECT_PER_QHEAD))
+    cache, _ = pooled_cache(a, 2)
+    table = i32(np.random.default_rng(1).integers(0, 200, (4, maxb)).tolist())
+    q = torch.randn(4, Hq, d, device="cuda").to(T[dtype])
+    out = []
+    for p in (a, b):
+        ws = sa.paged_workspace(p, ops=[sa.SA_OP_PAGED_DECODE])
+        out.append(sa.paged_decode(p, q, cache, table, i32(lens), ws))
+        done(ws)
+    assert all(torch.equal(x, y) for x, y in zip(*out))
