@@ -108,7 +108,9 @@ cudaError_t launch_paged_simt(const PagedShape &s, const void *q, const int32_t 
 // cu it takes packed chunks (no lists): the sequences of up to
 // paged_rows_limit rows a kv-head (0: none, INT_MAX: all of them).
 bool paged_decode_supported(const PagedShape &s);
-int paged_rows_limit(const PagedShape &s);
+// `least`: the lowest limit that a call has whose shape differs in its tables'
+// length only.
+int paged_rows_limit(const PagedShape &s, bool least = false);
 size_t paged_decode_scratch(const PagedShape &s, bool chunk);
 cudaError_t launch_paged_decode(const PagedShape &s, const void *q, const int32_t *cu, const PagedCache &c,
                                 const PagedLists &l, void *o, float *lse, unsigned *status, void *scratch,

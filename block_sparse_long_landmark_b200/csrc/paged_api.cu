@@ -83,7 +83,7 @@ size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op) {
         case SA_OP_PAGED_DECODE: return kStatusBytes + al256(paged_decode_scratch(s, false));
         case SA_OP_PAGED_PREFILL: {
             // one kernel after the other, in the same place
-            const int few = paged_rows_limit(s);
+            const int few = paged_rows_limit(s, true);
             const size_t rows = few > 0 ? paged_decode_scratch(s, true) : 0;
             const size_t tiles = few < INT_MAX && s.tokens > 0 && paged_prefill_supported(s) ? paged_prefill_scratch(s) : 0;
             return kStatusBytes + al256(rows > tiles ? rows : tiles);

@@ -972,13 +972,17 @@ long long rows_per_list(const PagedShape &s, bool chunk) {
 }
 int head_tiles(const PagedShape &s, bool chunk) { return rows_per_list(s, chunk) <= 8 ? 1 : 2; }
 int rows_per_group(const PagedShape &s, bool chunk) { return chunk ? 8 * head_tiles(s, true) : 16; }
+// A chunk call of few rows, on average (16 a sequence) and in all (1024).
+bool few_in_all(const PagedShape &s) {
+    return (long long)s.tokens * s.G <= max(256, min(16 * s.B, 1024));
+}
 // The most units a call can have: a chunk's rows are shared out over the
 // sequences on the device.
 long long units_of(const PagedShape &s, bool chunk) {
     const int group = rows_per_group(s, chunk);
     if (!chunk) return (long long)s.B * s.Hsel * ((s.heads_per + group - 1) / group);
     const long long any = (long long)s.tokens * s.G / group + s.B;
-    const int limit = paged_rows_limit(s);
+    const int limit = few_in_all(s) ? INT_MAX : paged_rows_limit(s, true);
     return min(any, limit == INT_MAX ? any : (long long)s.B * ((limit + group - 1) / group)) * s.Hkv;
 }
 size_t rec_bytes(const PagedShape &s, bool chunk) {
@@ -1027,16 +1031,26 @@ bool paged_decode_supported(const PagedShape &s) {
 // Most calls run both kernels, each over its own sequences: 512 + 63 x 1 tokens
 // over 64 x 16K keys take 542 us, all of them here 1090, all in tiles 1685.  The
 // tile kernel's three launches cost up to 20 us when no sequence is theirs (64 x
-// 4 tokens at 4000 keys 144 us with, 123 without), so a call of few rows, on
-// average (16) and in all (1024: what one long chunk among them can cost), runs
-// here as a whole.
-int paged_rows_limit(const PagedShape &s) {
+// 4 tokens at 4000 keys 146 us with, 131 without), so a call of few rows runs
+// here as a whole, as long as a chunk that hides in it cannot read too much
+// again: all the rows may be one sequence's, and that as long as its table, so
+// the bytes of those passes are held to 512 MB, about 80 us, four times what
+// the launches cost.  With tables for 128K keys, as a whole and by both kernels:
+// 63 + 1 tokens at 128K 755 and 304 us, 192 at 128K + 64 x 1 at 2K 2138 and 533,
+// 897 + 127 x 1 of one head a kv-head 3328 and 697; where no chunk hides, 64 x 4
+// tokens at 4000 keys 131 and 146, 8 x 5 at 5000 62 and 76.
+// `least`: as with the longest tables.
+int paged_rows_limit(const PagedShape &s, bool least) {
     constexpr int kFew = 40;
+    constexpr long long kHidden = 512ll << 20;
     const long long rows = (long long)s.tokens * s.G;
     if (s.dtype != SA_BF16 || s.tokens <= 0 || rows >= (1ll << 30)) return 0;
     if (s.G > 128) return INT_MAX;
-    if (s.B == 1) return rows <= kFew ? INT_MAX : 0;
-    return rows <= max(256, min(16 * s.B, 1024)) ? INT_MAX : kFew;
+    if (rows <= kFew) return INT_MAX;
+    if (s.B == 1) return 0;
+    const int group = rows_per_group(s, true);
+    const long long pass = 2ll * s.maxb * s.bs * s.Hkv * s.d;    // bytes of the longest sequence
+    return few_in_all(s) && !least && (rows + group - 1) / group <= kHidden / pass ? INT_MAX : kFew;
 }
 
 size_t paged_decode_scratch(const PagedShape &shape, bool chunk) {

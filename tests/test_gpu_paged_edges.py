@@ -352,3 +352,41 @@ def test_dense_decode_of_lists_per_query_head(dtype, d, block, Hq, Hkv):
         out.append(sa.paged_decode(p, q, cache, table, i32(lens), ws))
         done(ws)
     assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+# ---- which kernel a chunk call runs ----------------------------------------------------------
+
+def launches_of(B, tokens, Hq, Hkv, block, max_blocks, grown, lens):
+    p = sa.make_paged_params(B, Hq, Hkv, 128, block, 64, max_blocks, tokens, flags=sa.SA_CAUSAL)
+    cache, kv = pooled_cache(p, 2)
+    table = np.random.default_rng(1).integers(0, 64, (B, max_blocks)).astype(np.int32)
+    cu = [sum(grown[:i]) for i in range(B + 1)]
+    Q = torch.randn(tokens, Hq, 128, dtype=torch.float32).bfloat16()
+    ws = sa.paged_workspace(p, ops=[sa.SA_OP_PAGED_PREFILL])
+    torch.cuda.synchronize()
+    n = sa.sparse_attn_launch_count()
+    O, lse = sa.paged_prefill(p, Q.cuda(), i32(cu), cache, i32(table.tolist()), i32(lens), ws)
+    n = sa.sparse_attn_launch_count() - n
+    done(ws)
+    for b in range(B):
+        for t in {0, grown[b] - 1} & set(range(grown[b])):
+            see, h = lens[b] - grown[b] + t + 1, (b + t) % Hq
+            ref = op.decode_row(Q[cu[b] + t, h].double().numpy() * 128 ** -0.5, *kv, table[b], see, h // (Hq // Hkv), block, 0)
+            floor = 2.0 ** -32 * np.abs(op.rows_of(kv[1], table[b], see, h // (Hq // Hkv), block)).sum(0)
+            check_close("bf16", O[cu[b] + t, h], lse[cu[b] + t, h], ref, see, 128, floor, (b, t, h))
+    return n
+
+
+@pytest.mark.parametrize("B,grown", [(2, [63, 1]), (2, [0, 63]), (65, [192] + [1] * 64), (128, [897] + [1] * 127)])
+def test_a_long_chunk_beside_single_tokens_goes_to_the_tiles(B, grown):
+    """Tables for 128K keys: a chunk's rows, hidden in a call of few rows, are
+    not taken 8 or 16 at a time over its whole cache."""
+    G = 1 if B == 128 else 4
+    lens = [max(1000, grown[0] + 100)] + [300 + b for b in range(1, B)]
+    assert launches_of(B, sum(grown), 2 * G, 2, 64, 2048, grown, lens) == 5
+
+
+@pytest.mark.parametrize("B,grown,max_blocks", [(2, [5, 5], 2048), (8, [5] * 8, 79), (64, [1] * 64, 4)])
+def test_few_rows_stay_in_the_decodes_steps(B, grown, max_blocks):
+    """Up to 40 rows in all, or what a hidden chunk can read again is little."""
+    assert launches_of(B, sum(grown), 8, 2, 64, max_blocks, grown, [200 + b % 50 for b in range(B)]) == 2

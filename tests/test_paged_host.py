@@ -21,3 +21,13 @@ def _size(op, **kw):
 def test_a_decode_with_lists_per_query_head_has_room_for_one_without_lists(Hq, Hkv):
     f = sa.SA_SELECT_PER_QHEAD
     assert _size(sa.SA_OP_PAGED_DECODE, Hq=Hq, Hkv=Hkv, flags=f) >= _size(sa.SA_OP_PAGED_DECODE, Hq=Hq, Hkv=Hkv)
+
+
+@pytest.mark.parametrize("B,tokens", [(1, 9), (1, 30), (2, 64), (8, 40), (64, 256), (64, 257), (300, 4000), (2, 0)])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 8), (8, 8), (264, 2)])
+def test_a_chunk_calls_workspace_is_not_sized_by_the_tables(B, tokens, Hq, Hkv):
+    """Which kernels a call runs depends on the tables' length, what it needs does not."""
+    kw = dict(B=B, tokens=tokens, Hq=Hq, Hkv=Hkv)
+    sizes = {_size(sa.SA_OP_PAGED_PREFILL, max_blocks=m, pages=n, block=b, **kw)
+             for m, n, b in ((1, 1, 16), (8, 64, 64), (2048, 64, 64), (1 << 16, 1 << 14, 128))}
+    assert len(sizes) == 1 and min(sizes) >= 256
