@@ -422,7 +422,7 @@ paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__
             top = max(max(red[0], red[1]), max(red[2], red[3]));
         }
         const float am = __uint_as_float(top);
-        const bool usable = was >= 1.17549435e-38f && was <= 3.402823466e38f;
+        const bool usable = was > 0.f && was <= 3.402823466e38f;
         const bool fits = off > 0 && usable && am <= kMost * was;
         const float now = fits ? was : scale_for<kCode>(am);
         Sum8<kCode> sum;
@@ -596,7 +596,7 @@ paged_append_step_kernel(PagedShape s, const T *__restrict__ K, const T *__restr
         top = __reduce_max_sync(~0u, top);
     }
     const float am = __uint_as_float(top);
-    const bool usable = was >= 1.17549435e-38f && was <= 3.402823466e38f;
+    const bool usable = was > 0.f && was <= 3.402823466e38f;
     const bool fits = off > 0 && usable && am <= kMost * was;
     const float now = fits ? was : scale_for<kCode>(am);
     Sum8<kCode> sum;

@@ -390,3 +390,30 @@ def test_a_long_chunk_beside_single_tokens_goes_to_the_tiles(B, grown):
 def test_few_rows_stay_in_the_decodes_steps(B, grown, max_blocks):
     """Up to 40 rows in all, or what a hidden chunk can read again is little."""
     assert launches_of(B, sum(grown), 8, 2, 64, max_blocks, grown, [200 + b % 50 for b in range(B)]) == 2
+
+
+# ---- scales of other makers ----------------------------------------------------------------
+
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_append_to_subnormal_scales(code, few):
+    """What a page holds at a scale under 2^-126 is kept, or rounded anew to the scale that grows."""
+    pages, Hkv, d, block, held = (6, 2, 64, 32, 7) if few else (6 * 200, 8, 64, 32, 7)
+    p = sa.make_paged_params(pages, Hkv, Hkv, d, block, pages, 1, 2 * pages, code=code, dtype="fp32")
+    assert (2 * p.tokens * Hkv <= 64 * sms()) == few
+    rng = np.random.default_rng(5)
+    codes = [op.encode(p.code, rng.standard_normal((pages, Hkv, block, d)) * 40) for _ in "kv"]
+    scale = [np.resize([2.0 ** -127, 2.0 ** -130, 2.0 ** -133 * 5], (pages, Hkv)) for _ in "kv"]
+    x = [rng.choice([0.0, 2.0 ** -125, 2.0 ** -122, 2.0 ** -120], (pages, 1, 1, 1)) * rng.choice([0, 1, -1], (pages, 2, Hkv, d)) for _ in "kv"]
+    x = [y.reshape(2 * pages, Hkv, d) for y in x]
+    cache, ws = cache_of(p, codes, scale), sa.paged_workspace(p)
+    assert all(np.array_equal(c.double().cpu().numpy(), s) for c, s in zip(cache[2:], scale))
+    slot = [b * block + held + i for b in range(pages) for i in range(2)]
+    sa.paged_append(p, *(torch.from_numpy(y.astype(np.float32)).cuda() for y in x), torch.tensor(slot, device="cuda"), cache, ws)
+    done(ws)
+    for i in range(2):
+        was = scale[i].copy()
+        op.append(p.code, block, x[i], slot, codes[i], scale[i])
+        assert 0 < (scale[i] != was).mean() < 1
+        assert np.array_equal(cache[2 + i].double().cpu().numpy(), scale[i]), i
+        assert np.array_equal(raw(cache[i]), codes[i]), i
