@@ -269,17 +269,53 @@ __device__ __forceinline__ uint2 encode8(const float *y, float inv) {
     }
     return c;
 }
+// A value rounded to odd: v, rounded towards 0, with its last bit set where
+// something is left (`rest`, exact value minus v).  Rounding on to a code's few
+// bits is then one rounding of the exact value; from a v rounded to nearest it
+// is not, where that lies on the border between two codes.
+__device__ __forceinline__ float to_odd(float v, float rest) {
+    return __uint_as_float(__float_as_uint(v) | (rest != 0.f ? 1u : 0u));
+}
 // The same for any values and any scale: NaN becomes 0, what is beyond M (an
-// infinity) the largest code.
+// infinity) the largest code.  Out of line, as it is rare and its division
+// takes registers from the path that is not.
 template <int kCode>
-__device__ uint2 encode8_any(const float *y, float scale) {
+__device__ __noinline__ uint2 encode8_any(const float *y, float scale) {
     constexpr float kMost = kCode == SA_E4M3 ? 448.f : 127.f;
-    float v[8];
-    for (int i = 0; i < 8; ++i) {
-        const float q = __fdiv_rn(y[i], scale);
-        v[i] = isnan(q) ? 0.f : fminf(fmaxf(q, -kMost), kMost);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = y[2 * i + e], q = __fdiv_rz(x, scale);
+            v[e] = isnan(q) ? 0.f : fabsf(q) >= kMost ? copysignf(kMost, q) : to_odd(q, fmaf(-q, scale, x));
+        }
+        w[i] = codes_of2<kCode>(v[0], v[1]);
     }
-    return encode8<kCode>(v, 1.f);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+// Codes at a scale of `ratio` times the new one to codes at the new one.
+template <int kCode>
+__device__ __forceinline__ uint2 recode8(uint2 c, float ratio) {
+    if constexpr (kCode == SA_INT8) {
+        float y[8];
+        code_values4<kCode>(c.x, y);
+        code_values4<kCode>(c.y, y + 4);
+        return encode8<kCode>(y, ratio);        // multiplies and rounds at once
+    } else {
+        auto word = [&](uint32_t w) {
+            float y[4];
+            code_values4<kCode>(w, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = __fmul_rz(y[e], ratio);
+                y[e] = to_odd(p, fmaf(y[e], ratio, -p));
+            }
+            return codes_of2<kCode>(y[0], y[1]) | codes_of2<kCode>(y[2], y[3]) << 16;
+        };
+        return make_uint2(word(c.x), word(c.y));
+    }
 }
 
 // Last index b in [0, n) with off[b] <= x, found by a whole warp, 32 probes a
@@ -301,9 +337,10 @@ __device__ __forceinline__ int warp_owner(const int *off, int n, int x) {
 // the landmark the codes already in the block, are read into registers once:
 // their largest magnitude decides the scale (kept when the rows fit, else the
 // power of two that holds them, and the codes already there are rounded anew;
-// scales are powers of two, so a scaled value is exact and a code is one
-// rounding of it), then the codes are written and the mean of the block's
-// cached keys becomes its landmark.  A prompt's 30.6K tokens of 8 heads, int8:
+// a power of two divides exactly, so a code is one rounding of the value, and a
+// scale of another kind, kept from elsewhere, is divided by so that it stays
+// one), then the codes are written and the mean of the block's cached keys
+// becomes its landmark.  A prompt's 30.6K tokens of 8 heads, int8:
 // 54 us, 29 at the copy rate (two bytes in, one out per value); bound by issue
 // slots (73 % used by eight CTAs an SM).
 template <typename T, int kCode, int kD, int kRows>
@@ -432,13 +469,8 @@ paged_append_kernel(PagedShape s, const T *__restrict__ K, const T *__restrict__
             const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
 #pragma unroll 1
             for (int r = rs; r < off; r += RS) {
-                uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD), c = *at;
-                float y[8];
-                code_values4<kCode>(c.x, y);
-                code_values4<kCode>(c.y, y + 4);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= ratio;
-                c = encode8<kCode>(y, 1.f);
+                uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD);
+                const uint2 c = recode8<kCode>(*at, ratio);
                 *at = c;
                 if (mean) sum.add(c);
             }
@@ -605,13 +637,8 @@ paged_append_step_kernel(PagedShape s, const T *__restrict__ K, const T *__restr
         const float ratio = off > 0 && usable ? __fdiv_rn(was, now) : 0.f;
 #pragma unroll 1
         for (int r = rs; r < off; r += RS) {
-            uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD), c = *at;
-            float y[8];
-            code_values4<kCode>(c.x, y);
-            code_values4<kCode>(c.y, y + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= ratio;
-            c = encode8<kCode>(y, 1.f);
+            uint2 *at = reinterpret_cast<uint2 *>(blk + (size_t)r * kD);
+            const uint2 c = recode8<kCode>(*at, ratio);
             *at = c;
             if (mean) sum.add(c);
         }

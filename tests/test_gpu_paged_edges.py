@@ -417,3 +417,62 @@ def test_append_to_subnormal_scales(code, few):
         assert 0 < (scale[i] != was).mean() < 1
         assert np.array_equal(cache[2 + i].double().cpu().numpy(), scale[i]), i
         assert np.array_equal(raw(cache[i]), codes[i]), i
+
+def near_tie_scales(code, rng, n):
+    """fp32 scales below 1 and, for each, a code c such that c * scale is next
+    to a border between two codes of scale 1."""
+    t, c = (rng.choice(np.arange(8, 16) + 0.5, n), 2 * rng.integers(8, 16, n)) if code == "e4m3" else (
+        rng.choice(np.arange(0, 60) + 0.5, n), rng.integers(65, 128, n))
+    return (t / c).astype(np.float32), c
+
+
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,d,block", [("bf16", 128, 64), ("fp32", 64, 32), ("fp32", 128, 128), ("bf16", 64, 16)])
+def test_append_to_scales_that_are_no_powers_of_two(dtype, d, block, code, few):
+    """Pages filled elsewhere: a scale that is kept divides the new rows, one
+    that grows is divided by a power of two, and either is one rounding, next
+    to the border between two codes too; one old scale is 0."""
+    rng = np.random.default_rng(d + block)
+    pages, Hkv = (8, 2) if few else (600, 8)
+    held, new = 5, 3
+    p = sa.make_paged_params(pages, Hkv, Hkv, d, block, pages, 1, pages * new, dtype=dtype, code=code)
+    assert (2 * p.tokens * Hkv <= 64 * sms()) == few
+    M, c8 = op.MOST[p.code], p.code
+    codes, scale, x = [], [], []
+    for _ in "kv":
+        raw8 = op.encode(c8, rng.standard_normal((pages, Hkv, block, d)) * 30)
+        s, c = near_tie_scales(code, rng, pages * Hkv)
+        s, c = s.reshape(pages, Hkv), c.reshape(pages, Hkv)
+        raw8[..., :held, :8] = op.encode(c8, c[..., None, None].astype(float))
+        # heads in turn: kept, grown, kept, grown
+        y = rng.standard_normal((pages, new, Hkv, d))
+        for h in range(Hkv):
+            if h % 2 == 0:
+                ties = rng.choice(np.arange(8, 16) + 0.5 if code == "e4m3" else np.arange(0, 100) + 0.5, (pages, new, d))
+                y[:, :, h] = ties * s[:, h, None, None].astype(np.float64) * rng.choice([1, -1], (pages, new, d))
+            else:
+                y[:, :, h] = np.clip(y[:, :, h], -3.5, 3.5)
+                y[:, 0, h, 0] = M                                # the scale becomes 1
+        s[1, 0] = 0.0
+        codes.append(raw8)
+        scale.append(s.astype(np.float64))
+        x.append(torch.from_numpy(y.reshape(pages * new, Hkv, d)).to(T[dtype]))
+    cache, ws = cache_of(p, codes, scale), sa.paged_workspace(p)
+    slot = [page * block + held + i for page in range(pages) for i in range(new)]
+    L = torch.zeros(pages, Hkv, 1, d, dtype=T[dtype], device="cuda")
+    sa.paged_append(p, x[0].cuda(), x[1].cuda(), torch.tensor(slot, device="cuda"), cache, ws,
+                    cu=i32([new * b for b in range(pages + 1)]), new_len=i32([held + new] * pages), L=L)
+    done(ws)
+    grown = 0
+    for i in range(2):
+        was = scale[i].copy()
+        op.append(c8, block, x[i].double().numpy(), slot, codes[i], scale[i])
+        grown += (scale[i] != was).sum()
+        assert np.array_equal(cache[2 + i].double().cpu().numpy(), scale[i]), i
+        got = raw(cache[i])
+        assert np.array_equal(got, codes[i]), (i, (got != codes[i]).sum())
+    assert 0.4 < grown / (2 * pages * Hkv) < 0.6
+    ref = op.values(c8, codes[0], scale[0])[:, :, :held + new].mean(2)
+    tol = (torch.finfo(T[dtype]).eps / 2 + 3 * 2.0 ** -24) * np.abs(ref) + 2.0 ** -24 * M * scale[0][..., None]
+    assert (np.abs(L[:, :, 0].double().cpu().numpy() - ref) <= tol).all()
