@@ -123,7 +123,11 @@ paged_tables_kernel(PagedShape s, const int32_t *__restrict__ cur, const int32_t
         table[(size_t)b * s.maxb + (cur[b] + bs - 1) / bs + ((int)i - offA[b])] = popped((int)i);
     }
     // what stays released goes on the stack (above every entry that is popped)
-    for (long long i = first; i < R - A; i += step) free_pages[nf + i] = released((int)i);
+    for (long long i = first; i < R - A; i += step) {
+        const int pg = released((int)i);
+        if (pg < 0 || pg >= s.pages) set_status(status, kStatusBadIndex);
+        free_pages[nf + i] = pg;
+    }
     for (long long i = first; i < s.tokens; i += step) {
         long long out_slot = -1;
         if (i < T) {

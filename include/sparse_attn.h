@@ -482,7 +482,9 @@ size_t sparse_attn_paged_workspace_size(const sa_paged_params *p, int op);
  *                             the rows behind the last one
  * When the pages or the `tokens` slots do not suffice (status bit 16), or a
  * length or n_free is out of range (bit 1), nothing is given or taken:
- * n_free_out = n_free, cu = 0, every slot -1. */
+ * n_free_out = n_free, cu = 0, every slot -1.  A page out of 0 .. pages - 1
+ * that is given back or taken sets bit 1 too: given back it goes on the stack
+ * as it is, taken it is a table entry and slots of -1. */
 int sparse_attn_paged_tables(const sa_paged_params *p, const int32_t *cur_len, const int32_t *new_len,
                              int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int32_t *table,
                              int32_t *cu, int64_t *slot, void *ws, size_t ws_bytes, void *stream);

@@ -476,3 +476,21 @@ def test_append_to_scales_that_are_no_powers_of_two(dtype, d, block, code, few):
     ref = op.values(c8, codes[0], scale[0])[:, :, :held + new].mean(2)
     tol = (torch.finfo(T[dtype]).eps / 2 + 3 * 2.0 ** -24) * np.abs(ref) + 2.0 ** -24 * M * scale[0][..., None]
     assert (np.abs(L[:, :, 0].double().cpu().numpy() - ref) <= tol).all()
+
+
+# ---- pages given back -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", [-1, 8, -2 ** 31, 2 ** 31 - 1])
+def test_tables_report_a_bad_page_that_is_given_back(bad):
+    """Where it is given back, not in the step that pops it."""
+    p = sa.make_paged_params(2, 1, 1, 64, 16, 8, 4, 10)
+    ws = sa.paged_workspace(p, ops=[sa.SA_OP_PAGED_TABLES])
+    table = i32([[1, bad, 3, -1], [5, -1, -1, -1]])
+    free, n_free = i32([0, 2, 4, 6, 7, 0, 0, 0]), i32([5])
+    n, cu, slot = sa.paged_tables(p, i32([40, 3]), i32([10, 4]), free, n_free, table, ws)
+    torch.cuda.synchronize()
+    assert sa.sparse_attn_check_status(ws.data_ptr(), 0) == (sa.SA_ERR_DEVICE, 1)
+    assert n.item() == 7 and free[5:7].tolist() == [bad, 3] and slot.tolist() == [5 * 16 + 3] + [-1] * 9
+    # behind a sequence's last block anything may stand
+    n, cu, slot = sa.paged_tables(p, i32([10, 4]), i32([9, 5]), free, n, table, ws)
+    done(ws)
